@@ -310,7 +310,172 @@ mla_status_t mla_cache_quantize_fp8(const void *cache_bf16, const int32_t *block
                                     void *stream);
 
 /*
- * mla_cache_get_error - device error bits of the cache writers since the last
+ * mla_rope_freqs - angle per position of every rotated pair, for mla_rope and
+ * mla_cache_append_rope.  HOST function: writes rot / 2 doubles to the host
+ * array `freqs` (copy them to the device for the calls).  With
+ * theta_i = base^(-2i/rot), i < rot / 2:
+ *   MLA_ROPE_PLAIN   f_i = theta_i
+ *   MLA_ROPE_LINEAR  f_i = theta_i / factor               (position interpolation)
+ *   MLA_ROPE_NTK     f_i = (base * factor^(rot/(rot-2)))^(-2i/rot): the fastest pair
+ *                    keeps its angle, the slowest is slowed by `factor`
+ *   MLA_ROPE_YARN    pairs that turn more than beta_fast times over the original
+ *                    context orig_len keep theta_i, pairs that turn fewer than
+ *                    beta_slow times get theta_i / factor, with a linear ramp between
+ *                    ("YaRN: Efficient Context Window Extension of Large Language
+ *                    Models", NTK-by-parts): with pair(n) = rot * ln(orig_len /
+ *                    (2 pi n)) / (2 ln base), lo = max(0, floor(pair(beta_fast))),
+ *                    hi = min(rot - 1, ceil(pair(beta_slow))), r_i = clamp((i - lo) /
+ *                    max(hi - lo, 0.001), 0, 1):
+ *                    f_i = theta_i (1 - r_i) + theta_i / factor * r_i
+ * rot: even, 2..256; base > 1; factor >= 1 and finite; orig_len > 0 and beta_fast >=
+ * beta_slow > 0 (MLA_ROPE_YARN only, ignored otherwise).  factor = 1 gives theta_i in
+ * every mode.  MLA_ROPE_NTK needs rot >= 4.
+ */
+typedef enum {
+    MLA_ROPE_PLAIN = 0,
+    MLA_ROPE_LINEAR = 1,
+    MLA_ROPE_NTK = 2,
+    MLA_ROPE_YARN = 3
+} mla_rope_scaling_t;
+
+mla_status_t mla_rope_freqs(int rot, double base, mla_rope_scaling_t scaling, double factor,
+                            double orig_len, double beta_fast, double beta_slow, double *freqs);
+
+/* Layout flags of the rotation (mla_rope, mla_cache_append_rope). */
+#define MLA_ROPE_INTERLEAVED 0x0u /* pair i = elements (2i, 2i + 1) */
+#define MLA_ROPE_HALF        0x1u /* pair i = elements (i, i + rot/2) */
+#define MLA_ROPE_INVERSE     0x2u /* rotate by the negative angle */
+
+/*
+ * mla_rope - rotary positions of T tokens with H heads each: every pair (a, b) of the
+ * rot rotated elements of x[t,h] becomes, with c = mscale cos(pos[t] f_i) and
+ * s = mscale sin(pos[t] f_i) (s negated by MLA_ROPE_INVERSE),
+ *     (a c - b s,  a s + b c)
+ * so that a score depends on the distance of two positions only.  x, y: bf16; element
+ * r of head h of token t is x[t*x_ldt + h*x_ldh + r], r < rot (strides in elements), so
+ * the rotated part of a longer head ([nope | rope] rows) is a pointer to its first
+ * element, and y can be the last 64 columns of the packed [T,H,576] query that
+ * mla_absorb_q writes (pass it q_rope = NULL).  Elements outside the rot rotated ones
+ * are not touched.  y = x with equal strides rotates in place; y must not overlap x in
+ * any other way, nor two of its own rows each other.
+ * pos: int32 [T] (any value); freqs: f64 [rot/2] from mla_rope_freqs, on the device;
+ * mscale: finite.  The angle is formed and reduced in double, so far positions keep
+ * their accuracy; the rotation is fp32, rounded once.  The inverse rotation with the
+ * same mscale is also the gradient of y with respect to x.
+ * T >= 0 (0 is a no-op), 1 <= H <= 65535, rot even in 2..256, strides >= 0;
+ * x, y 2-byte, pos 4-byte and freqs 8-byte aligned.  Rows whose pointers and strides are
+ * multiples of 16 bytes, with rot a multiple of 16, are moved 16 bytes at a time.
+ */
+mla_status_t mla_rope(const void *x, long long x_ldt, long long x_ldh, const int32_t *pos,
+                      const double *freqs, float mscale, unsigned flags, void *y,
+                      long long y_ldt, long long y_ldh, int T, int H, int rot, void *stream);
+
+/*
+ * mla_cache_append_rope - mla_cache_append for tokens whose position is not their slot
+ * (a cache that mla_cache_evict compacted) or whose rotation is scaled or laid out
+ * differently:
+ *     cache[block_table[b,s/64], s%64, :] = [c_kv[t] | R(k_r[t], pos[t])],  s = slot[t]
+ * with b = seq_idx[t] and R the rotation of mla_rope (rot = 64; freqs f64 [32]).
+ * c_kv: bf16 rows of stride ckv_ld elements (>= 512, a multiple of 8, 16-byte aligned);
+ * k_r: bf16 rows of stride kr_ld elements (>= 64, even, 4-byte aligned): both may be
+ * columns of one [T,576] projection.  slot_pos: int32 [B, 64*max_blocks_per_seq] or
+ * NULL; if given, slot_pos[b,s] = pos[t] is recorded for mla_cache_evict.  Errors as
+ * for mla_cache_append (mla_cache_get_error).  T = 0 is a no-op.
+ */
+mla_status_t mla_cache_append_rope(const void *c_kv, int ckv_ld, const void *k_r, int kr_ld,
+                                   const int32_t *seq_idx, const int32_t *slot,
+                                   const int32_t *pos, int T, const double *freqs, float mscale,
+                                   unsigned flags, const int32_t *block_table, int B,
+                                   int max_blocks_per_seq, int num_blocks, void *cache,
+                                   int32_t *slot_pos, void *stream);
+
+/*
+ * mla_chunk_workspace_bytes - bytes of device workspace mla_chunk_attend needs for T
+ * query tokens of B sequences with H heads and `num_splits` split-KV partitions (0 = the
+ * automatic count of the current device).  Returns 0 on invalid arguments.
+ */
+size_t mla_chunk_workspace_bytes(int T, int B, int H, int num_splits);
+
+/*
+ * mla_chunk_attend - attention of ragged chunks of new tokens over the paged latent
+ * cache (prefill of a prompt in chunks, mixed batches): mla_decode_multi for any number
+ * of tokens per sequence.  The queries of sequence b are tokens q_offsets[b] ..
+ * q_offsets[b+1] - 1 of q; their own rows are already in the cache, as its last rows.
+ * With n = q_offsets[b+1] - q_offsets[b], token j of them attends to the first
+ * seq_lens[b] - (n - 1 - j) cached tokens.
+ * q: bf16 [T,H,576]; q_offsets: int32 [B+1] on the device, non-decreasing, in 0..T;
+ * out: bf16 [T,H,512]; lse: f32 [T,H].  Tokens before q_offsets[0] or at and past
+ * q_offsets[B] are neither read nor written.  A token that sees no cached token gives
+ * out = 0 and lse = -inf.  cache, block_table, seq_lens, softmax_scale, num_splits,
+ * workspace (mla_chunk_workspace_bytes; 256-byte aligned, zero-filled before its first
+ * use, one call at a time) and the error bits (mla_get_device_error) as for mla_decode,
+ * bf16 cache; a sequence whose offsets decrease or leave 0..T records
+ * MLA_DEVERR_SEQ_TOO_LONG and its tokens are not written.
+ * T >= 0 (0 is a no-op), T * H <= 2^30.
+ */
+mla_status_t mla_chunk_attend(const void *q, const int32_t *q_offsets, int T, const void *cache,
+                              const int32_t *block_table, const int32_t *seq_lens, int B, int H,
+                              int num_blocks, int max_blocks_per_seq, float softmax_scale,
+                              void *out, float *lse, void *workspace, size_t workspace_bytes,
+                              int num_splits, void *stream);
+
+/*
+ * mla_cache_weigh - the attention weight every cached token received, accumulated over
+ * heads and queries (what mla_cache_evict ranks tokens by): for t < seq_lens[b]
+ *     weight_out[b,t] = weight_in[b,t] + sum_{j,h} exp(scale q[j,h] . row_t - lse[j,h])
+ * over the n tokens j of sequence b (q_offsets as for mla_chunk_attend) that see t, i.e.
+ * t < seq_lens[b] - (n - 1 - j); lse is mla_decode's or mla_chunk_attend's for the same
+ * queries and cache, so every query adds probabilities that sum to 1 per head.
+ * q: bf16 [T,H,576]; lse: f32 [T,H] (+inf: the row adds nothing); bf16 cache;
+ * weight_in, weight_out: f32 [B, 64*max_blocks_per_seq], slot order; weight_in may be
+ * NULL (zeros) or weight_out itself, and must not overlap it otherwise.  Slots at and
+ * past seq_lens[b] are not written.  The sum is fp32 in an order that depends on the
+ * shapes alone.  Bad block ids, lengths and offsets are recorded for
+ * mla_cache_get_error; a token whose block id is bad keeps its weight_in.  T >= 0,
+ * T * H <= 2^30.
+ */
+mla_status_t mla_cache_weigh(const void *q, const int32_t *q_offsets, int T, const float *lse,
+                             const void *cache, const int32_t *block_table,
+                             const int32_t *seq_lens, int B, int H, int num_blocks,
+                             int max_blocks_per_seq, float softmax_scale, const float *weight_in,
+                             float *weight_out, void *stream);
+
+/*
+ * mla_evict_workspace_bytes - bytes of device workspace mla_cache_evict needs.  Returns
+ * 0 on invalid arguments.
+ */
+size_t mla_evict_workspace_bytes(int B, int max_blocks_per_seq);
+
+/*
+ * mla_cache_evict - cut every sequence of the bf16 cache to its budget and compact it.
+ * Sequence b keeps n = min(max(keep[b], 0), seq_lens[b]) tokens: the first ones in the
+ * order (protected before others, larger weight first, lower slot first), a slot being
+ * protected when slot_pos < n_first or slot_pos > (largest slot_pos of the sequence) -
+ * n_recent.  A NaN weight ranks as -inf.  Kept tokens in slots below n stay where they
+ * are; the k-th kept token behind them moves into the k-th free slot below n, row,
+ * weight and position.  Attention does not depend on the order of cached rows (every
+ * key carries its own rotation), so the fewest rows move.
+ * weight: f32, slot_pos: int32, both [B, 64*max_blocks_per_seq]; keep, seq_lens: int32
+ * [B]; new_weight, new_pos, new_lens: the same shapes, for the compacted sequences:
+ * slots n .. seq_lens[b] - 1 get weight 0 and position -1, slots past seq_lens[b] are
+ * not written.  new_weight, new_pos and new_lens may each be the corresponding input
+ * itself (and must not overlap the inputs otherwise).  The block table is not changed:
+ * the blocks from ceil(n / 64) on are free for reuse.  No block may be in two rows of
+ * the table, or twice in one, below the sequences' lengths (a shared prefix would be
+ * compacted for all its sequences).
+ * workspace: mla_evict_workspace_bytes(...), 256-byte aligned, zero-filled before its
+ * first use, one call at a time; error bits by mla_get_device_error (a row whose source
+ * or destination has a bad block id is not moved).
+ */
+mla_status_t mla_cache_evict(const float *weight, const int32_t *slot_pos,
+                             const int32_t *seq_lens, const int32_t *keep, int n_first,
+                             int n_recent, const int32_t *block_table, int B, int num_blocks,
+                             int max_blocks_per_seq, void *cache, float *new_weight,
+                             int32_t *new_pos, int32_t *new_lens, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/*
+ * mla_cache_get_error - device error bits of the cache writers and of mla_cache_weigh since the last
  * call; synchronises `stream` and clears them.  As for the absorption, the
  * word is one per device and process, shared by calls on every stream.
  * MLA_ERR_INVALID_ARG if err_bits is NULL.

@@ -33,7 +33,12 @@ EXPORTS = ("mla_absorb_q", "mla_absorb_o", "mla_absorb_get_error", "mla_cache_ap
            "mla_cache_quantize_fp8", "mla_cache_get_error", "mla_set_wait_limit", "mla_decode_multi",
            "mla_decode_workspace_bytes", "mla_decode_fp8_workspace_bytes", "mla_decode",
            "mla_combine", "mla_get_device_error", "mla_status_string", "mla_num_sms",
-           "mla_decode_noalloc", "mla_decode_noalloc_get_error", "mla_last_error_string")
+           "mla_decode_noalloc", "mla_decode_noalloc_get_error", "mla_last_error_string",
+           "mla_rope_freqs", "mla_rope", "mla_cache_append_rope", "mla_chunk_workspace_bytes",
+           "mla_chunk_attend", "mla_cache_weigh", "mla_evict_workspace_bytes", "mla_cache_evict")
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+ROPE_LAYOUT = {"interleaved": 0x0, "half": 0x1}
+ROPE_INVERSE = 0x2
 
 
 class MLAError(RuntimeError):
@@ -97,6 +102,28 @@ def load():
                                          ctypes.c_float, vp, vp, i32, vp]
         L.mla_decode_noalloc_get_error.restype = i32
         L.mla_decode_noalloc_get_error.argtypes = [vp, vp]
+        f64, i64 = ctypes.c_double, ctypes.c_longlong
+        L.mla_rope_freqs.restype = i32
+        L.mla_rope_freqs.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp]
+        L.mla_rope.restype = i32
+        L.mla_rope.argtypes = [vp, i64, i64, vp, vp, ctypes.c_float, ctypes.c_uint, vp, i64, i64,
+                               i32, i32, i32, vp]
+        L.mla_cache_append_rope.restype = i32
+        L.mla_cache_append_rope.argtypes = [vp, i32, vp, i32, vp, vp, vp, i32, vp, ctypes.c_float,
+                                            ctypes.c_uint, vp, i32, i32, i32, vp, vp, vp]
+        L.mla_chunk_workspace_bytes.restype = u64
+        L.mla_chunk_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.mla_chunk_attend.restype = i32
+        L.mla_chunk_attend.argtypes = [vp, vp, i32, vp, vp, vp, i32, i32, i32, i32, ctypes.c_float,
+                                       vp, vp, vp, u64, i32, vp]
+        L.mla_cache_weigh.restype = i32
+        L.mla_cache_weigh.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32,
+                                      ctypes.c_float, vp, vp, vp]
+        L.mla_evict_workspace_bytes.restype = u64
+        L.mla_evict_workspace_bytes.argtypes = [i32, i32]
+        L.mla_cache_evict.restype = i32
+        L.mla_cache_evict.argtypes = [vp, vp, vp, vp, i32, i32, vp, i32, i32, i32, vp, vp, vp, vp,
+                                      vp, u64, vp]
         _lib = L
         return L
 
@@ -343,6 +370,188 @@ def mla_get_device_error(workspace, stream=None) -> int:
     _check("mla_get_device_error",
            load().mla_get_device_error(_ptr(workspace), _stream(stream), ctypes.byref(v)))
     return int(v.value)
+
+
+def _same_device(first, *others):
+    """All tensors on the first one's device, which must be the current one
+    (the C entry points launch on the current device)."""
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    if first.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {first.device}, current device cuda:{torch.cuda.current_device()}")
+
+
+def _need_rows(t, name, dim, width=None):
+    """bf16 CUDA rows with a contiguous last axis; other strides are free."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != dim or (width is not None and t.shape[-1] != width):
+        raise ValueError(f"{name}: expected {dim} axes" + (f", the last of {width}" if width else "")
+                         + f", got {tuple(t.shape)}")
+    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+
+
+def _rope_flags(layout, inverse=False):
+    if layout not in ROPE_LAYOUT:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUT)}, got {layout!r}")
+    return ROPE_LAYOUT[layout] | (ROPE_INVERSE if inverse else 0)
+
+
+def mla_rope_freqs(rot=64, base=10000.0, scaling="none", factor=1.0, orig_len=4096.0,
+                   beta_fast=32.0, beta_slow=1.0, device="cuda") -> torch.Tensor:
+    """Angle per position of each of the rot/2 pairs (f64, on ``device``): plain
+    or scaled for long contexts ("linear", "ntk", "yarn"; see include/mla.h)."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALING)}, got {scaling!r}")
+    host = (ctypes.c_double * max(1, int(rot) // 2))()
+    _check("mla_rope_freqs", load().mla_rope_freqs(int(rot), float(base), ROPE_SCALING[scaling], float(factor),
+                                                   float(orig_len), float(beta_fast), float(beta_slow), host))
+    return torch.tensor(list(host), dtype=torch.float64, device=device)
+
+
+def mla_rope(x, pos, freqs, y, *, mscale=1.0, layout="interleaved", inverse=False, stream=None):
+    """y[t,h] = x[t,h] rotated by pos[t] * freqs.  x, y: [T,H,rot] bf16 views whose
+    last axis is contiguous (e.g. the last columns of longer rows); y may be x."""
+    _need_rows(x, "x", 3)
+    T, H, rot = (int(v) for v in x.shape)
+    _need_rows(y, "y", 3, rot)
+    if y.shape != x.shape:
+        raise ValueError(f"y: expected shape {tuple(x.shape)}, got {tuple(y.shape)}")
+    _need(pos, "pos", torch.int32, (T,))
+    _need(freqs, "freqs", torch.float64, (rot // 2,))
+    _same_device(x, pos, freqs, y)
+    _check("mla_rope", load().mla_rope(_ptr(x), x.stride(0), x.stride(1), _ptr(pos), _ptr(freqs), float(mscale),
+                                       _rope_flags(layout, inverse), _ptr(y), y.stride(0), y.stride(1), T, H, rot,
+                                       _stream(stream)))
+    return y
+
+
+def mla_cache_append_rope(c_kv, k_r, seq_idx, slot, pos, freqs, block_table, cache, *, slot_pos=None,
+                          mscale=1.0, layout="interleaved", stream=None):
+    """Write [c_kv | rotated k_r] rows of new tokens into slots of the paged bf16
+    cache, rotated at ``pos`` (which need not be the slot)."""
+    _need_rows(c_kv, "c_kv", 2, 512)
+    T = int(c_kv.shape[0])
+    _need_rows(k_r, "k_r", 2, 64)
+    if int(k_r.shape[0]) != T:
+        raise ValueError(f"k_r: expected {T} rows, got {int(k_r.shape[0])}")
+    for t, name in ((seq_idx, "seq_idx"), (slot, "slot"), (pos, "pos")):
+        _need(t, name, torch.int32, (T,))
+    _need(freqs, "freqs", torch.float64, (32,))
+    B, mb, NB = _need_paged(cache, block_table)
+    if slot_pos is not None:
+        _need(slot_pos, "slot_pos", torch.int32, (B, 64 * mb))
+    _same_device(c_kv, k_r, seq_idx, slot, pos, freqs, block_table, cache, slot_pos)
+    ckv_ld = c_kv.stride(0) if T > 1 else max(512, c_kv.stride(0) // 8 * 8)
+    kr_ld = k_r.stride(0) if T > 1 else max(64, k_r.stride(0) // 2 * 2)
+    _check("mla_cache_append_rope", load().mla_cache_append_rope(
+        _ptr(c_kv), ckv_ld, _ptr(k_r), kr_ld, _ptr(seq_idx), _ptr(slot), _ptr(pos), T, _ptr(freqs), float(mscale),
+        _rope_flags(layout), _ptr(block_table), B, mb, NB, _ptr(cache), _ptr(slot_pos), _stream(stream)))
+    return cache
+
+
+def _need_paged(cache, block_table):
+    """Checks a bf16 paged cache and its table; returns (B, max_blocks, num_blocks)."""
+    _need(cache, "cache", torch.bfloat16)
+    if cache.dim() != 3 or tuple(cache.shape[1:]) != (64, 576):
+        raise ValueError("bf16 cache must be [num_blocks,64,576]")
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B,max_blocks]")
+    return int(block_table.shape[0]), int(block_table.shape[1]), int(cache.shape[0])
+
+
+def mla_chunk_workspace_bytes(T: int, B: int, H: int, num_splits: int = 0) -> int:
+    return int(load().mla_chunk_workspace_bytes(int(T), int(B), int(H), int(num_splits)))
+
+
+def alloc_chunk_workspace(T: int, B: int, H: int, num_splits: int = 0, device=None) -> torch.Tensor:
+    """Zero-filled device workspace of the size mla_chunk_attend needs."""
+    n = mla_chunk_workspace_bytes(T, B, H, num_splits)
+    if n == 0:
+        raise MLAError("mla_chunk_workspace_bytes", 1)
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _need_chunk(q, q_offsets, cache, block_table, seq_lens):
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [T,H,576] tensor")
+    T, H = int(q.shape[0]), int(q.shape[1])
+    _need(q, "q", torch.bfloat16, (T, H, 576))
+    B, mb, NB = _need_paged(cache, block_table)
+    _need(q_offsets, "q_offsets", torch.int32, (B + 1,))
+    _need(seq_lens, "seq_lens", torch.int32, (B,))
+    return T, H, B, mb, NB
+
+
+def mla_chunk_attend(q, q_offsets, cache, block_table, seq_lens, softmax_scale, out, lse, workspace, *,
+                     num_splits=0, stream=None):
+    """Attention of ragged chunks of new tokens (q [T,H,576], sequence b owning
+    tokens q_offsets[b]..q_offsets[b+1]-1) over the paged bf16 cache."""
+    T, H, B, mb, NB = _need_chunk(q, q_offsets, cache, block_table, seq_lens)
+    _need(out, "out", torch.bfloat16, (T, H, 512))
+    _need(lse, "lse", torch.float32, (T, H))
+    _need(workspace, "workspace", torch.uint8)
+    _same_device(q, q_offsets, cache, block_table, seq_lens, out, lse, workspace)
+    _check("mla_chunk_attend", load().mla_chunk_attend(
+        _ptr(q), _ptr(q_offsets), T, _ptr(cache), _ptr(block_table), _ptr(seq_lens), B, H, NB, mb,
+        float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), int(workspace.numel()), int(num_splits),
+        _stream(stream)))
+    return out, lse
+
+
+def mla_cache_weigh(q, q_offsets, lse, cache, block_table, seq_lens, softmax_scale, weight, weight_out, *,
+                    stream=None):
+    """weight_out = weight (or 0 if None) + the attention probability every cached
+    token received from the queries, summed over heads and tokens."""
+    T, H, B, mb, NB = _need_chunk(q, q_offsets, cache, block_table, seq_lens)
+    _need(lse, "lse", torch.float32, (T, H))
+    if weight is not None:
+        _need(weight, "weight", torch.float32, (B, 64 * mb))
+    _need(weight_out, "weight_out", torch.float32, (B, 64 * mb))
+    _same_device(q, q_offsets, lse, cache, block_table, seq_lens, weight, weight_out)
+    _check("mla_cache_weigh", load().mla_cache_weigh(
+        _ptr(q), _ptr(q_offsets), T, _ptr(lse), _ptr(cache), _ptr(block_table), _ptr(seq_lens), B, H, NB, mb,
+        float(softmax_scale), _ptr(weight), _ptr(weight_out), _stream(stream)))
+    return weight_out
+
+
+def mla_evict_workspace_bytes(B: int, max_blocks: int) -> int:
+    return int(load().mla_evict_workspace_bytes(int(B), int(max_blocks)))
+
+
+def alloc_evict_workspace(B: int, max_blocks: int, device=None) -> torch.Tensor:
+    """Zero-filled device workspace of the size mla_cache_evict needs."""
+    n = mla_evict_workspace_bytes(B, max_blocks)
+    if n == 0:
+        raise MLAError("mla_evict_workspace_bytes", 1)
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def mla_cache_evict(weight, slot_pos, seq_lens, keep, n_first, n_recent, block_table, cache, new_weight, new_pos,
+                    new_lens, workspace, *, stream=None):
+    """Cut every sequence to its ``keep`` best tokens and compact the cache;
+    new_weight, new_pos and new_lens may be the inputs themselves."""
+    B, mb, NB = _need_paged(cache, block_table)
+    for t, name in ((weight, "weight"), (new_weight, "new_weight")):
+        _need(t, name, torch.float32, (B, 64 * mb))
+    for t, name in ((slot_pos, "slot_pos"), (new_pos, "new_pos")):
+        _need(t, name, torch.int32, (B, 64 * mb))
+    for t, name in ((seq_lens, "seq_lens"), (keep, "keep"), (new_lens, "new_lens")):
+        _need(t, name, torch.int32, (B,))
+    _need(workspace, "workspace", torch.uint8)
+    _same_device(weight, slot_pos, seq_lens, keep, block_table, cache, new_weight, new_pos, new_lens, workspace)
+    _check("mla_cache_evict", load().mla_cache_evict(
+        _ptr(weight), _ptr(slot_pos), _ptr(seq_lens), _ptr(keep), int(n_first), int(n_recent), _ptr(block_table), B,
+        NB, mb, _ptr(cache), _ptr(new_weight), _ptr(new_pos), _ptr(new_lens), _ptr(workspace),
+        int(workspace.numel()), _stream(stream)))
+    return new_lens, new_weight, new_pos
 
 
 # ----------------------------------------------------------------------------

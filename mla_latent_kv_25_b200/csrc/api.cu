@@ -147,6 +147,18 @@ bool valid_rows(int rows) {
   return valid_heads(rows) || (rows > kMaxHeads && rows <= kMaxTiledRows && rows % kMaxHeads == 0);
 }
 
+bool misaligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
+
+bool valid_rot(int rot) { return rot >= 2 && rot <= 256 && rot % 2 == 0; }
+bool valid_table(int max_blocks) { return max_blocks >= 1 && max_blocks <= (1 << 24); }
+
+// Query tokens of a ragged call: row numbers T * H stay int32 (TMA coordinates).
+constexpr int kMaxTokens = 1 << 26;
+bool valid_chunk(int T, int B, int H) {
+  return T >= 0 && T <= kMaxTokens && B >= 1 && B <= kMaxBatch && valid_heads(H) &&
+         static_cast<long long>(T) * H <= (1LL << 30);
+}
+
 }  // namespace
 
 extern "C" {
@@ -267,9 +279,12 @@ mla_status_t mla_cache_quantize_fp8(const void* cache_bf16, const int32_t* block
 mla_status_t mla_cache_get_error(void* stream, uint32_t* err_bits) {
   if (!err_bits) return MLA_ERR_INVALID_ARG;
   uint32_t v = 0;
+  uint32_t w = 0;
   if (cudaError_t e = cache_take_error(&v, static_cast<cudaStream_t>(stream)); e != cudaSuccess)
     return cuda_fail(e);
-  *err_bits = v;
+  if (cudaError_t e = weigh_take_error(&w, static_cast<cudaStream_t>(stream)); e != cudaSuccess)
+    return cuda_fail(e);
+  *err_bits = v | w;
   return MLA_OK;
 }
 
@@ -464,6 +479,217 @@ mla_status_t mla_get_device_error(void* workspace, void* stream, uint32_t* err_b
     if (cudaError_t e = cudaStreamSynchronize(st); e != cudaSuccess) return cuda_fail(e);
   }
   return MLA_OK;
+}
+
+mla_status_t mla_rope_freqs(int rot, double base, mla_rope_scaling_t scaling, double factor,
+                            double orig_len, double beta_fast, double beta_slow, double* freqs) {
+  if (!freqs || !valid_rot(rot)) return MLA_ERR_INVALID_ARG;
+  if (!(base > 1.0) || isinf(base) || !(factor >= 1.0) || isinf(factor)) return MLA_ERR_INVALID_ARG;
+  switch (scaling) {
+    case MLA_ROPE_PLAIN:
+    case MLA_ROPE_LINEAR: break;
+    case MLA_ROPE_NTK:
+      if (rot < 4) return MLA_ERR_INVALID_ARG;
+      base *= pow(factor, rot / (rot - 2.0));
+      break;
+    case MLA_ROPE_YARN:
+      if (!(orig_len > 0.0) || isinf(orig_len) || !(beta_slow > 0.0) || !(beta_fast >= beta_slow) || isinf(beta_fast))
+        return MLA_ERR_INVALID_ARG;
+      break;
+    default: return MLA_ERR_INVALID_ARG;
+  }
+  const double two_pi = 6.283185307179586476925286766559;
+  auto pair = [&](double turns) { return rot * log(orig_len / (turns * two_pi)) / (2.0 * log(base)); };
+  double lo = 0.0, hi = 0.0;
+  if (scaling == MLA_ROPE_YARN) {
+    lo = fmax(0.0, floor(pair(beta_fast)));
+    hi = fmin(rot - 1.0, ceil(pair(beta_slow)));
+  }
+  for (int i = 0; i < rot / 2; ++i) {
+    const double theta = pow(base, -2.0 * i / rot);
+    double f = theta;
+    if (scaling == MLA_ROPE_LINEAR) f = theta / factor;
+    if (scaling == MLA_ROPE_YARN) {
+      const double r = fmin(1.0, fmax(0.0, (i - lo) / fmax(hi - lo, 1e-3)));
+      f = theta * (1.0 - r) + theta / factor * r;
+    }
+    freqs[i] = f;
+  }
+  return MLA_OK;
+}
+
+mla_status_t mla_rope(const void* x, long long x_ldt, long long x_ldh, const int32_t* pos,
+                      const double* freqs, float mscale, unsigned flags, void* y, long long y_ldt,
+                      long long y_ldh, int T, int H, int rot, void* stream) {
+  if (T < 0 || T > kMaxTokens || H < 1 || H > 65535 || !valid_rot(rot)) return MLA_ERR_INVALID_ARG;
+  if ((flags & ~(MLA_ROPE_HALF | MLA_ROPE_INVERSE)) != 0 || !isfinite(mscale)) return MLA_ERR_INVALID_ARG;
+  if (x_ldt < 0 || x_ldh < 0 || y_ldt < 0 || y_ldh < 0) return MLA_ERR_INVALID_ARG;
+  if (T == 0) return MLA_OK;
+  if (!x || !pos || !freqs || !y) return MLA_ERR_INVALID_ARG;
+  if (misaligned(x, 2) || misaligned(y, 2) || misaligned(pos, 4) || misaligned(freqs, 8)) return MLA_ERR_INVALID_ARG;
+  // rows of y on top of each other would be written twice
+  if ((H > 1 && y_ldh < rot) || (T > 1 && y_ldt < rot)) return MLA_ERR_INVALID_ARG;
+  RopeParams p;
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.y = static_cast<__nv_bfloat16*>(y);
+  // a stride that no second token or head uses does not count for alignment
+  p.x_ldt = T > 1 ? x_ldt : 0;
+  p.y_ldt = T > 1 ? y_ldt : 0;
+  p.x_ldh = H > 1 ? x_ldh : 0;
+  p.y_ldh = H > 1 ? y_ldh : 0;
+  p.pos = pos;
+  p.freqs = freqs;
+  p.mscale = mscale;
+  p.flags = flags;
+  p.T = T;
+  p.H = H;
+  p.rot = rot;
+  return status_of(launch_rope(p, device_sms(), static_cast<cudaStream_t>(stream)));
+}
+
+mla_status_t mla_cache_append_rope(const void* c_kv, int ckv_ld, const void* k_r, int kr_ld,
+                                   const int32_t* seq_idx, const int32_t* slot, const int32_t* pos,
+                                   int T, const double* freqs, float mscale, unsigned flags,
+                                   const int32_t* block_table, int B, int max_blocks_per_seq,
+                                   int num_blocks, void* cache, int32_t* slot_pos, void* stream) {
+  if (T < 0 || T > kMaxBatch * 64 || B < 1 || B > kMaxBatch || num_blocks < 1 || !valid_table(max_blocks_per_seq))
+    return MLA_ERR_INVALID_ARG;
+  if ((flags & ~(MLA_ROPE_HALF | MLA_ROPE_INVERSE)) != 0 || !isfinite(mscale)) return MLA_ERR_INVALID_ARG;
+  if (ckv_ld < kDc || ckv_ld % 8 != 0 || kr_ld < kDr || kr_ld % 2 != 0) return MLA_ERR_INVALID_ARG;
+  if (T == 0) return MLA_OK;
+  if (!c_kv || !k_r || !seq_idx || !slot || !pos || !freqs || !block_table || !cache) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(c_kv) || !aligned16(cache) || misaligned(k_r, 4) || misaligned(seq_idx, 4) || misaligned(slot, 4) ||
+      misaligned(pos, 4) || misaligned(freqs, 8) || misaligned(block_table, 4) || misaligned(slot_pos, 4))
+    return MLA_ERR_INVALID_ARG;
+  AppendRopeParams p;
+  p.c_kv = static_cast<const __nv_bfloat16*>(c_kv);
+  p.k_r = static_cast<const __nv_bfloat16*>(k_r);
+  p.ckv_ld = ckv_ld;
+  p.kr_ld = kr_ld;
+  p.seq_idx = seq_idx;
+  p.slot = slot;
+  p.pos = pos;
+  p.T = T;
+  p.freqs = freqs;
+  p.mscale = mscale;
+  p.flags = flags;
+  p.block_table = block_table;
+  p.B = B;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.cache = static_cast<__nv_bfloat16*>(cache);
+  p.slot_pos = slot_pos;
+  return status_of(launch_cache_append_rope(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t mla_chunk_workspace_bytes(int T, int B, int H, int num_splits) {
+  if (!valid_chunk(T, B, H) || num_splits < 0 || num_splits > kMaxSplits) return 0;
+  return 256;
+}
+
+mla_status_t mla_chunk_attend(const void* q, const int32_t* q_offsets, int T, const void* cache,
+                              const int32_t* block_table, const int32_t* seq_lens, int B, int H,
+                              int num_blocks, int max_blocks_per_seq, float softmax_scale, void* out,
+                              float* lse, void* workspace, size_t workspace_bytes, int num_splits,
+                              void* stream) {
+  if (!valid_chunk(T, B, H) || num_blocks < 1 || !valid_table(max_blocks_per_seq)) return MLA_ERR_INVALID_ARG;
+  if (num_splits < 0 || num_splits > kMaxSplits || !isfinite(softmax_scale)) return MLA_ERR_INVALID_ARG;
+  if (T == 0) return MLA_OK;
+  if (!q || !q_offsets || !cache || !block_table || !seq_lens || !out || !lse || !workspace) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || misaligned(lse, 4) || misaligned(q_offsets, 4) ||
+      misaligned(block_table, 4) || misaligned(seq_lens, 4) || misaligned(workspace, 256))
+    return MLA_ERR_INVALID_ARG;
+  if (workspace_bytes < mla_chunk_workspace_bytes(T, B, H, num_splits)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  ChunkParams p;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_offsets = q_offsets;
+  p.cache = static_cast<const __nv_bfloat16*>(cache);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.T = T;
+  p.B = B;
+  p.H = H;
+  p.num_blocks = num_blocks;
+  p.max_blocks = max_blocks_per_seq;
+  p.softmax_scale = softmax_scale;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.err = static_cast<uint32_t*>(workspace);
+  return status_of(launch_chunk_simple(p, static_cast<cudaStream_t>(stream)));
+}
+
+mla_status_t mla_cache_weigh(const void* q, const int32_t* q_offsets, int T, const float* lse,
+                             const void* cache, const int32_t* block_table, const int32_t* seq_lens,
+                             int B, int H, int num_blocks, int max_blocks_per_seq,
+                             float softmax_scale, const float* weight_in, float* weight_out,
+                             void* stream) {
+  if (!valid_chunk(T, B, H) || num_blocks < 1 || !valid_table(max_blocks_per_seq)) return MLA_ERR_INVALID_ARG;
+  if (!isfinite(softmax_scale)) return MLA_ERR_INVALID_ARG;
+  if (!q_offsets || !cache || !block_table || !seq_lens || !weight_out) return MLA_ERR_INVALID_ARG;
+  if (T > 0 && (!q || !lse)) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(cache) || misaligned(lse, 4) || misaligned(q_offsets, 4) ||
+      misaligned(block_table, 4) || misaligned(seq_lens, 4) || misaligned(weight_in, 4) || misaligned(weight_out, 4))
+    return MLA_ERR_INVALID_ARG;
+  WeighParams p;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_offsets = q_offsets;
+  p.lse = lse;
+  p.cache = static_cast<const __nv_bfloat16*>(cache);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.T = T;
+  p.B = B;
+  p.H = H;
+  p.num_blocks = num_blocks;
+  p.max_blocks = max_blocks_per_seq;
+  p.softmax_scale = softmax_scale;
+  p.weight_in = weight_in;
+  p.weight_out = weight_out;
+  return status_of(launch_weigh(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t mla_evict_workspace_bytes(int B, int max_blocks_per_seq) {
+  if (B < 1 || B > kMaxBatch || !valid_table(max_blocks_per_seq)) return 0;
+  return evict_layout(B, max_blocks_per_seq).total;
+}
+
+mla_status_t mla_cache_evict(const float* weight, const int32_t* slot_pos, const int32_t* seq_lens,
+                             const int32_t* keep, int n_first, int n_recent,
+                             const int32_t* block_table, int B, int num_blocks,
+                             int max_blocks_per_seq, void* cache, float* new_weight,
+                             int32_t* new_pos, int32_t* new_lens, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (!weight || !slot_pos || !seq_lens || !keep || !block_table || !cache || !new_weight || !new_pos || !new_lens ||
+      !workspace)
+    return MLA_ERR_INVALID_ARG;
+  if (B < 1 || B > kMaxBatch || num_blocks < 1 || !valid_table(max_blocks_per_seq) || n_first < 0 || n_recent < 0)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(cache) || misaligned(weight, 4) || misaligned(slot_pos, 4) || misaligned(seq_lens, 4) ||
+      misaligned(keep, 4) || misaligned(block_table, 4) || misaligned(new_weight, 4) || misaligned(new_pos, 4) ||
+      misaligned(new_lens, 4) || misaligned(workspace, 256))
+    return MLA_ERR_INVALID_ARG;
+  const EvictLayout lay = evict_layout(B, max_blocks_per_seq);
+  if (workspace_bytes < lay.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  uint8_t* wsb = static_cast<uint8_t*>(workspace);
+  EvictParams p;
+  p.weight = weight;
+  p.slot_pos = slot_pos;
+  p.seq_lens = seq_lens;
+  p.keep = keep;
+  p.n_first = n_first;
+  p.n_recent = n_recent;
+  p.block_table = block_table;
+  p.B = B;
+  p.num_blocks = num_blocks;
+  p.max_blocks = max_blocks_per_seq;
+  p.cache = static_cast<__nv_bfloat16*>(cache);
+  p.new_weight = new_weight;
+  p.new_pos = new_pos;
+  p.new_lens = new_lens;
+  p.err = reinterpret_cast<uint32_t*>(wsb);
+  p.n_moves = reinterpret_cast<int32_t*>(wsb + lay.n_moves);
+  p.moves = reinterpret_cast<int2*>(wsb + lay.moves);
+  return status_of(launch_evict(p, device_sms(), static_cast<cudaStream_t>(stream)));
 }
 
 const char* mla_last_error_string(void) { return g_last_error; }

@@ -11,6 +11,10 @@
 //   i.  The angle is formed and reduced modulo 2 pi in double, so long
 //   positions keep their accuracy; the rotation itself is fp32.
 //
+// cache_append_rope_kernel: the same for a position that is not the slot and
+//   for scaled or half-layout rotations (rope.cuh); source rows may be columns
+//   of a longer row.
+//
 // cache_quantize_fp8_kernel: one CTA per listed block converts the bf16
 //   cache block to the fp8 layout: codes = c_kv / scale rounded to E4M3
 //   (nearest, saturating), scale = amax / 448 (1 for an all-zero block), both
@@ -20,6 +24,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "rope.cuh"
 
 namespace mla {
 
@@ -65,6 +70,39 @@ cache_append_kernel(const __nv_bfloat16* __restrict__ c_kv, const __nv_bfloat16*
   const float x0 = __bfloat162float(x.x), x1 = __bfloat162float(x.y);
   reinterpret_cast<__nv_bfloat162*>(row + kDc)[lane] =
       __floats2bfloat162_rn(x0 * c - x1 * s, x0 * s + x1 * c);
+}
+
+__global__ void __launch_bounds__(32 * kAppendWarps) cache_append_rope_kernel(const AppendRopeParams p) {
+  const int t = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (t >= p.T) return;
+  const int b = p.seq_idx[t];
+  const int s = p.slot[t];
+  if (b < 0 || b >= p.B || s < 0 || s >= p.max_blocks * kBlock) {
+    if (lane == 0) atomicOr(&g_cache_err, kErrSeqTooLong);
+    return;
+  }
+  const int blk = p.block_table[size_t(b) * p.max_blocks + s / kBlock];
+  if (blk < 0 || blk >= p.num_blocks) {
+    if (lane == 0) atomicOr(&g_cache_err, kErrBadBlock);
+    return;
+  }
+  const uint4* src = reinterpret_cast<const uint4*>(p.c_kv + size_t(t) * p.ckv_ld);
+  const uint4 v0 = src[lane], v1 = src[lane + 32];
+  // lane i owns pair i
+  const bool half = (p.flags & kRopeHalf) != 0;
+  const int ia = half ? lane : 2 * lane, ib = half ? lane + 32 : 2 * lane + 1;
+  const __nv_bfloat16* key = p.k_r + size_t(t) * p.kr_ld;
+  float a = __bfloat162float(key[ia]), c = __bfloat162float(key[ib]);
+  const int at = p.pos[t];
+  rope_pair(a, c, rope_factors(at, p.freqs[lane], p.mscale, (p.flags & kRopeInverse) != 0));
+  __nv_bfloat16* row = p.cache + (size_t(blk) * kBlock + s % kBlock) * kRow;
+  uint4* dst = reinterpret_cast<uint4*>(row);
+  dst[lane] = v0;
+  dst[lane + 32] = v1;
+  row[kDc + ia] = __float2bfloat16_rn(a);
+  row[kDc + ib] = __float2bfloat16_rn(c);
+  if (lane == 0 && p.slot_pos != nullptr) p.slot_pos[size_t(b) * p.max_blocks * kBlock + s] = at;
 }
 
 constexpr int kQuantThreads = 256;
@@ -132,6 +170,12 @@ cudaError_t launch_cache_append(const __nv_bfloat16* c_kv, const __nv_bfloat16* 
   const int grid = (T + kAppendWarps - 1) / kAppendWarps;
   cache_append_kernel<<<grid, 32 * kAppendWarps, 0, stream>>>(c_kv, k_r, seq_idx, pos, T, block_table,
                                                               B, max_blocks, num_blocks, cache);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_append_rope(const AppendRopeParams& p, cudaStream_t stream) {
+  const int grid = (p.T + kAppendWarps - 1) / kAppendWarps;
+  cache_append_rope_kernel<<<grid, 32 * kAppendWarps, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -76,6 +76,85 @@ cudaError_t launch_fp8_widen(const uint8_t* codes, const __nv_bfloat16* k_rope,
                              const int32_t* seq_lens, int B, int max_blocks, int num_blocks,
                              int32_t* wide_table, __nv_bfloat16* wide_cache, uint32_t* err,
                              int num_sms, cudaStream_t stream);
+struct RopeParams {
+  const __nv_bfloat16* x;
+  __nv_bfloat16* y;
+  long long x_ldt, x_ldh, y_ldt, y_ldh;  // strides in elements
+  const int32_t* pos;                    // [T]
+  const double* freqs;                   // [rot/2]
+  float mscale;
+  unsigned flags;
+  int T, H, rot;
+};
+cudaError_t launch_rope(const RopeParams& p, int num_sms, cudaStream_t stream);
+
+struct AppendRopeParams {
+  const __nv_bfloat16* c_kv;
+  const __nv_bfloat16* k_r;
+  int ckv_ld, kr_ld;
+  const int32_t* seq_idx;
+  const int32_t* slot;
+  const int32_t* pos;
+  int T;
+  const double* freqs;
+  float mscale;
+  unsigned flags;
+  const int32_t* block_table;
+  int B, max_blocks, num_blocks;
+  __nv_bfloat16* cache;
+  int32_t* slot_pos;  // [B, 64*max_blocks] or null
+};
+cudaError_t launch_cache_append_rope(const AppendRopeParams& p, cudaStream_t stream);
+
+// Ragged chunks of query tokens over the paged cache (mla_chunk_attend).
+struct ChunkParams {
+  const __nv_bfloat16* q;    // [T,H,576]
+  const int32_t* q_offsets;  // [B+1]
+  const __nv_bfloat16* cache;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int T, B, H, num_blocks, max_blocks;
+  float softmax_scale;
+  __nv_bfloat16* out;  // [T,H,512]
+  float* lse;          // [T,H]
+  uint32_t* err;
+};
+cudaError_t launch_chunk_simple(const ChunkParams& p, cudaStream_t stream);
+
+struct WeighParams {
+  const __nv_bfloat16* q;    // [T,H,576]
+  const int32_t* q_offsets;  // [B+1]
+  const float* lse;          // [T,H]
+  const __nv_bfloat16* cache;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int T, B, H, num_blocks, max_blocks;
+  float softmax_scale;
+  const float* weight_in;  // [B, 64*max_blocks] or null
+  float* weight_out;
+};
+cudaError_t launch_weigh(const WeighParams& p, cudaStream_t stream);
+// Copies mla_cache_weigh's error word to *bits and clears it (synchronises `stream`).
+cudaError_t weigh_take_error(uint32_t* bits, cudaStream_t stream);
+
+struct EvictParams {
+  const float* weight;      // [B, 64*max_blocks]
+  const int32_t* slot_pos;  // [B, 64*max_blocks]
+  const int32_t* seq_lens;
+  const int32_t* keep;
+  int n_first, n_recent;
+  const int32_t* block_table;
+  int B, num_blocks, max_blocks;
+  __nv_bfloat16* cache;
+  float* new_weight;
+  int32_t* new_pos;
+  int32_t* new_lens;
+  uint32_t* err;
+  int32_t* n_moves;  // [B]
+  int2* moves;       // [B, 32*max_blocks] (source slot, destination slot)
+};
+cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t stream);
+
 // Copies the cache writers' error word to *bits and clears it (synchronises `stream`).
 cudaError_t cache_take_error(uint32_t* bits, cudaStream_t stream);
 // Copies the absorption kernels' error word to *bits and clears it (synchronises `stream`).

@@ -64,4 +64,19 @@ inline Fp8Plan plan_fp8_groups(int B, int rows, int max_blocks, int P, size_t ws
   }
 }
 
+// Workspace of an eviction: error word, moves per sequence, move lists (at
+// most half of a sequence's slots are free below its budget and filled from
+// behind it).
+struct EvictLayout {
+  size_t n_moves, moves, total;
+};
+
+inline EvictLayout evict_layout(int B, int max_blocks) {
+  EvictLayout w;
+  w.n_moves = 256;
+  w.moves = align256(w.n_moves + size_t(B) * 4);
+  w.total = w.moves + size_t(B) * max_blocks * (kBlock / 2) * 8;
+  return w;
+}
+
 }  // namespace mla
