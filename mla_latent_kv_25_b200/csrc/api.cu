@@ -132,6 +132,14 @@ bool encode_bf16_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t
   return encode_bf16(map, base, 2, dims, strides, box);
 }
 
+// Query rows [rows, 576] in 64 x 128 boxes.
+bool encode_rows_map(CUtensorMap* map, const void* base, uint64_t rows) {
+  cuuint64_t dims[2] = {uint64_t(kRow), rows};
+  cuuint64_t strides[1] = {uint64_t(kRow) * 2};
+  cuuint32_t box[2] = {64, 128};
+  return encode_bf16(map, base, 2, dims, strides, box);
+}
+
 constexpr int kMaxBatch = 1 << 20;
 constexpr long long kDefaultSpin = 4000000000LL;  // ~2 s of SM clock
 std::atomic<long long> g_decode_wait_limit{kDefaultSpin};  // set by mla_set_wait_limit
@@ -645,7 +653,15 @@ mla_status_t mla_cache_weigh(const void* q, const int32_t* q_offsets, int T, con
   p.softmax_scale = softmax_scale;
   p.weight_in = weight_in;
   p.weight_out = weight_out;
-  return status_of(launch_weigh(p, static_cast<cudaStream_t>(stream)));
+  p.spin_limit = g_decode_wait_limit.load();
+  const int sms = device_sms();
+  if (sms < 1) return fail_with("no streaming multiprocessor count for the current device");
+  CUtensorMap qmap, kmap;
+  // without queries the map is never read through: any valid base does
+  if (!encode_rows_map(&qmap, T > 0 ? q : cache, T > 0 ? uint64_t(T) * H : 128) ||
+      !encode_bf16_map(&kmap, cache, uint64_t(num_blocks) * kBlock, kRow, kRow * 2))
+    return fail_with("tensor map encoding failed");
+  return status_of(launch_weigh(p, qmap, kmap, sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t mla_evict_workspace_bytes(int B, int max_blocks_per_seq) {

@@ -1,4 +1,4 @@
-// Chunk attention and attention weights on CUDA cores: the plain loops over
+// Chunk attention on CUDA cores: the plain loops over
 // the definition, fp32 throughout.
 #include <math.h>
 
@@ -6,8 +6,6 @@
 #include "kernels.h"
 
 namespace mla {
-
-__device__ uint32_t g_weigh_err;
 
 namespace {
 
@@ -124,43 +122,6 @@ __global__ void __launch_bounds__(kThreads) chunk_simple_kernel(const ChunkParam
   }
 }
 
-// grid (tiles of 32 slots, B): thread = (slot, one of 8 row shares)
-__global__ void __launch_bounds__(kThreads) weigh_simple_kernel(const WeighParams p) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  auto* k = reinterpret_cast<__nv_bfloat16(*)[kRow + 8]>(raw);
-  __shared__ int valid[kTile];
-  __shared__ float part[8][kTile];
-  const int b = blockIdx.y;
-  const int len = checked_len(p.seq_lens, b, p.max_blocks, &g_weigh_err);
-  const int a = p.q_offsets[b], e = p.q_offsets[b + 1];
-  const bool bad = a < 0 || e > p.T || e < a;
-  if (bad && threadIdx.x == 0) atomicOr(&g_weigh_err, kErrSeqTooLong);
-  const int n = bad ? 0 : e - a;
-  const size_t S = size_t(p.max_blocks) * kBlock;
-  for (int t0 = blockIdx.x * kTile; t0 < len; t0 += gridDim.x * kTile) {
-    __syncthreads();
-    stage(p.cache, p.block_table + size_t(b) * p.max_blocks, p.num_blocks, t0, len, k, valid, &g_weigh_err);
-    __syncthreads();
-    const int c = threadIdx.x % kTile, share = threadIdx.x / kTile;
-    float acc = 0.f;
-    for (int r = share; r < n * p.H; r += 8) {
-      if (!valid[c] || t0 + c >= len - (n - 1 - r / p.H)) continue;
-      const size_t row = size_t(a) * p.H + r;
-      const __nv_bfloat16* q = p.q + row * kRow;
-      float s = 0.f;
-      for (int d = 0; d < kRow; ++d) s += __bfloat162float(q[d]) * __bfloat162float(k[c][d]);
-      acc += expf(s * p.softmax_scale - p.lse[row]);
-    }
-    part[share][c] = acc;
-    __syncthreads();
-    if (threadIdx.x < kTile && t0 + c < len) {
-      float s = p.weight_in ? p.weight_in[b * S + t0 + c] : 0.f;
-      for (int i = 0; i < 8; ++i) s += part[i][c];
-      p.weight_out[b * S + t0 + c] = s;
-    }
-  }
-}
-
 }  // namespace
 
 cudaError_t launch_chunk_simple(const ChunkParams& p, cudaStream_t stream) {
@@ -170,21 +131,6 @@ cudaError_t launch_chunk_simple(const ChunkParams& p, cudaStream_t stream) {
     return e;
   chunk_simple_kernel<<<dim3(p.T, p.H / kRows), kThreads, smem, stream>>>(p);
   return cudaGetLastError();
-}
-
-cudaError_t launch_weigh(const WeighParams& p, cudaStream_t stream) {
-  const int smem = kTile * (kRow + 8) * 2;
-  weigh_simple_kernel<<<dim3(min(2 * p.max_blocks, 1024), p.B), kThreads, smem, stream>>>(p);
-  return cudaGetLastError();
-}
-
-cudaError_t weigh_take_error(uint32_t* bits, cudaStream_t stream) {
-  uint32_t* dev = nullptr;
-  cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void**>(&dev), g_weigh_err);
-  if (e != cudaSuccess) return e;
-  if ((e = cudaMemcpyAsync(bits, dev, sizeof(uint32_t), cudaMemcpyDeviceToHost, stream)) != cudaSuccess) return e;
-  if ((e = cudaMemsetAsync(dev, 0, sizeof(uint32_t), stream)) != cudaSuccess) return e;
-  return cudaStreamSynchronize(stream);
 }
 
 }  // namespace mla

@@ -132,8 +132,12 @@ struct WeighParams {
   float softmax_scale;
   const float* weight_in;  // [B, 64*max_blocks] or null
   float* weight_out;
+  long long spin_limit;
 };
-cudaError_t launch_weigh(const WeighParams& p, cudaStream_t stream);
+// qmap: q as [max(T, 1)*H, 576] with 64 x 128 boxes; kmap: the cache as
+// [num_blocks*64, 576] with 64 x 64 boxes; both 128-byte swizzled.
+cudaError_t launch_weigh(const WeighParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap, int num_sms,
+                         cudaStream_t stream);
 // Copies mla_cache_weigh's error word to *bits and clears it (synchronises `stream`).
 cudaError_t weigh_take_error(uint32_t* bits, cudaStream_t stream);
 
