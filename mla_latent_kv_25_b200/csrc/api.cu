@@ -96,6 +96,19 @@ int resolve_engines(int num_splits, int B) {
   return P;
 }
 
+// Engines of a chunk call: one per co-resident cluster of four SMs.
+int resolve_chunk_engines(int num_splits) {
+  if (num_splits > 0) return num_splits;
+  if (const int env = env_splits(); env > 0) return env;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  static std::mutex mu;
+  static int cache[64] = {0};
+  std::lock_guard<std::mutex> g(mu);
+  if (cache[dev] == 0) cache[dev] = chunk_sm100_max_clusters();
+  return cache[dev];
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -592,7 +605,8 @@ mla_status_t mla_cache_append_rope(const void* c_kv, int ckv_ld, const void* k_r
 
 size_t mla_chunk_workspace_bytes(int T, int B, int H, int num_splits) {
   if (!valid_chunk(T, B, H) || num_splits < 0 || num_splits > kMaxSplits) return 0;
-  return 256;
+  const int P = resolve_chunk_engines(num_splits);
+  return P < 1 ? 0 : chunk_layout(T, B, H, P).total;
 }
 
 mla_status_t mla_chunk_attend(const void* q, const int32_t* q_offsets, int T, const void* cache,
@@ -607,7 +621,10 @@ mla_status_t mla_chunk_attend(const void* q, const int32_t* q_offsets, int T, co
   if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || misaligned(lse, 4) || misaligned(q_offsets, 4) ||
       misaligned(block_table, 4) || misaligned(seq_lens, 4) || misaligned(workspace, 256))
     return MLA_ERR_INVALID_ARG;
-  if (workspace_bytes < mla_chunk_workspace_bytes(T, B, H, num_splits)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  const int P = resolve_chunk_engines(num_splits);
+  if (P < 1) return fail_with("no streaming multiprocessor count for the current device");
+  const ChunkLayout lay = chunk_layout(T, B, H, P);
+  if (workspace_bytes < lay.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
   ChunkParams p;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_offsets = q_offsets;
@@ -622,8 +639,22 @@ mla_status_t mla_chunk_attend(const void* q, const int32_t* q_offsets, int T, co
   p.softmax_scale = softmax_scale;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
-  p.err = static_cast<uint32_t*>(workspace);
-  return status_of(launch_chunk_simple(p, static_cast<cudaStream_t>(stream)));
+  p.P = P;
+  p.max_tiles = lay.max_tiles;
+  p.spin_limit = g_decode_wait_limit.load();
+  uint8_t* wsb = static_cast<uint8_t*>(workspace);
+  p.err = reinterpret_cast<uint32_t*>(wsb);
+  p.n_tiles = reinterpret_cast<int*>(wsb + lay.n_tiles);
+  p.tile_off = reinterpret_cast<int*>(wsb + lay.tile_off);
+  p.tiles = reinterpret_cast<int4*>(wsb + lay.tiles);
+  p.pre = reinterpret_cast<long long*>(wsb + lay.pre);
+  p.lse_part = reinterpret_cast<float*>(wsb + lay.lse_part);
+  p.o_part = reinterpret_cast<float*>(wsb + lay.o_part);
+  CUtensorMap qmap, kmap;
+  if (!encode_rows_map(&qmap, q, uint64_t(T) * H) ||
+      !encode_bf16_map(&kmap, cache, uint64_t(num_blocks) * kBlock, kRow, kRow * 2))
+    return fail_with("tensor map encoding failed");
+  return status_of(launch_chunk_sm100(p, kmap, qmap, static_cast<cudaStream_t>(stream)));
 }
 
 mla_status_t mla_cache_weigh(const void* q, const int32_t* q_offsets, int T, const float* lse,

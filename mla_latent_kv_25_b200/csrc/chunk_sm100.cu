@@ -1,0 +1,1109 @@
+// Attention of ragged chunks of new tokens over the paged latent cache on
+// sm_100a tensor cores.
+//
+// A tile is 256 query rows: as many whole tokens of one sequence as fit (2 at
+// H = 128).  One engine = a cluster of four CTAs, two pairs of SMs split by
+// role, because the fp32 output of 256 rows x 512 latent columns fills the
+// TMEM of two SMs:
+//
+//   score pair (ranks 0, 1)                     value pair (ranks 2, 3)
+//   S[256 x 256] = Q K^T, cta_group::2:         O[256 x 512] += P V, cta_group::2:
+//   each CTA holds 128 query rows in shared     each CTA holds P of 128 rows and half
+//   memory and half of the pass's 256 tokens;   of the latent columns of each block;
+//   S is double-buffered in TMEM                O fills TMEM
+//   w0 TMA of K, w2 TMA of Q, w1 MMA (rank 0)   w0 TMA of V, w1 MMA (rank 2), w2 zeroes
+//   w4-11 softmax of the CTA's 128 rows,        V rows past the length, w3 (rank 3)
+//         P by st.async to CTA rank + 2         relays P's arrival to rank 2,
+//                                               w4-11 rescale, output
+//
+// Bound: the tensor pipe, 2 * rows * tokens * (576 + 512) FLOPs.  Why this
+// shape: with 256 rows to a cached token a pair reads 576 bytes of K (512 of
+// V) per SM and token while its MMAs take 18 (16) cycles, 32 bytes per clock
+// and SM from L2; 128 rows on two SMs would need twice that.  M = 256, N = 256
+// is also the shape at which the pipe runs at its full rate.
+//
+// The tiles' blocks are laid end to end and cut into P equal ranges, one per
+// engine (as the decode does with sequences), so ragged batches balance and a
+// few tokens over a long context still use every SM; cut tiles are merged by
+// chunk_merge_kernel.  chunk_plan_kernel writes the tile list.
+//
+// Softmax as in the decode: fp32, a head row's running max moves only when a
+// pass exceeds it by 2^8, P is rounded to bf16 (relative error 2^-9, like
+// every bf16 input of a tensor-core product) while its sum is taken unrounded.
+// Every wait is bounded (WaitCtx).
+#include <cuda.h>
+#include <math.h>
+
+#include <atomic>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "pair.cuh"
+#include "plan.h"
+#include "sm100.cuh"
+
+namespace mla {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 384;
+constexpr int kTileRows = kChunkTileRows;     // 256
+constexpr int kPassBlocks = 4;                // blocks per QK pass (N = 256)
+constexpr int kChunks = kRow / 64;            // 64-column chunks of a row
+constexpr int kKSlots = 5;                    // score: ring of [128 tokens x 64] chunks
+constexpr int kVSlots = 4;                    // value: ring of [64 tokens x 256] half blocks
+constexpr int kNP = 5;                        // P records in flight
+
+constexpr uint32_t kQChunk = 128 * 128;       // [128 rows x 64] bf16
+constexpr uint32_t kBlkChunk = 64 * 128;      // [64 tokens x 64] bf16
+constexpr uint32_t kKSlot = 2 * kBlkChunk;
+constexpr uint32_t kVSlot = 4 * kBlkChunk;
+constexpr uint32_t kPBytes = 128 * 64 * 2;    // P [128 rows x 64 tokens] bf16, 8 x 8 core matrices
+constexpr uint32_t kPCoreK = 128 * 16;        // bytes per 8-token column of core matrices
+constexpr uint32_t kMetaBytes = 128 * 16;     // per row: alpha, m, l, unused
+constexpr uint32_t kFlagBytes = 64;           // per quadrant: rescale flag
+constexpr uint32_t kRecBytes = 19 * 1024;
+constexpr float kRescaleThreshold = 8.0f;     // log2 units
+constexpr float kLog2e = 1.4426950408889634f;
+static_assert(kPBytes + kMetaBytes + kFlagBytes <= kRecBytes, "record layout");
+constexpr uint32_t kTmemCols = 512;
+constexpr uint16_t kScoreMask = 0x3, kValueMask = 0xc;
+
+// Barriers live at the same offsets in all four CTAs; "leader" ones are used
+// in rank 0 (score) or rank 2 (value) only.
+struct Barriers {
+  uint64_t k_full[kKSlots];                    // leader: both CTAs' K chunks landed
+  uint64_t k_empty[kKSlots];                   // commit to both
+  uint64_t q_full[kChunks];                    // leader
+  uint64_t q_empty[kChunks];                   // commit to both
+  uint64_t s_full[2];                          // commit to both
+  uint64_t s_empty[2];                         // leader: all softmax warps of both
+  uint64_t xchg[4];                            // the two softmax threads of a row swap max / sum
+  uint64_t p_empty[kNP];                       // score CTAs: record r of the value CTA is free
+  uint64_t v_full[kVSlots];                    // this CTA's V landed
+  uint64_t v_ready[kVSlots];                   // leader: both CTAs' V landed and cleaned
+  uint64_t v_empty[kVSlots];                   // commit to both
+  uint64_t p_full[kNP];                        // this CTA's P record landed
+  uint64_t p_peer[kNP];                        // leader: the peer's record landed
+  uint64_t epi_req;                            // both: request posted + MMAs done
+  uint64_t corr_done, o_free;                  // leader: all epilogue warps of both
+  uint64_t meta_done;                          // all epilogue warps read the final record
+  uint32_t peer_flag[kNP];                     // leader: the peer record's rescale flags
+  uint32_t req;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(Barriers) <= 1024, "barrier block too large");
+
+constexpr uint32_t kXchgOff = 1024;            // score: float [2 buffers][2 halves][128]
+constexpr uint32_t kXchgBytes = 2 * 2 * 128 * 4;
+constexpr uint32_t kQOff = 3072;               // score: Q, nine chunks
+constexpr uint32_t kXchgEnd = kXchgOff + kXchgBytes;
+static_assert(kXchgEnd <= kQOff, "exchange buffers");
+__host__ __device__ constexpr uint32_t q_off(int ch) { return kQOff + ch * kQChunk; }
+__host__ __device__ constexpr uint32_t k_slot_off(int s) { return kQOff + kChunks * kQChunk + s * kKSlot; }
+__host__ __device__ constexpr uint32_t v_slot_off(int s) { return 1024 + s * kVSlot; }
+__host__ __device__ constexpr uint32_t rec_off(int r) { return 1024 + kVSlots * kVSlot + r * kRecBytes; }
+constexpr uint32_t kScoreSmem = k_slot_off(kKSlots);
+constexpr uint32_t kValueSmem = rec_off(kNP);
+// the dynamic shared memory of a kernel without static shared memory starts
+// at a multiple of 1024 here; the kernel checks it
+constexpr uint32_t kSmemBytes = kScoreSmem > kValueSmem ? kScoreSmem : kValueSmem;
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+__host__ __device__ constexpr uint32_t idesc_qk(int per) { return idesc_bf16(256, 128 * per, false, false); }
+constexpr uint32_t kIdescPV = idesc_bf16(256, 256, false, true);
+
+// ------------------------------------------------------------------ segments
+
+// One piece of a tile: blocks [blk_lo, blk_hi) of its sequence.
+struct Seg {
+  int row0, rows;  // first row of q / out, number of rows
+  int b;
+  int len;         // cached tokens that the tile's last query token sees
+  int blk_lo, blk_hi;
+  int slot;        // partial slot, or -1 when the piece is the whole tile
+};
+
+// Tile holding concatenated block x: the last t with pre[t] <= x and a block.
+__device__ __forceinline__ int tile_of(const long long* pre, int nt, long long x) {
+  int lo = 0, hi = nt;  // pre[lo] <= x < pre[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+struct Walker {
+  const ChunkParams* p;
+  long long s, e;
+  int t, nt, engine, count;
+
+  __device__ __noinline__ void init(const ChunkParams& pp, int engine_) {
+    p = &pp;
+    engine = engine_;
+    nt = *pp.n_tiles;
+    count = 0;
+    t = nt;
+    s = e = 0;
+    const long long total = pp.pre[nt];
+    const int P = total < pp.P ? static_cast<int>(total) : pp.P;
+    if (engine >= P) return;
+    s = range_start(engine, total, P);
+    e = range_start(engine + 1, total, P);
+    t = tile_of(pp.pre, nt, s);
+  }
+
+  __device__ __noinline__ bool next(Seg& g) {
+    while (t < nt) {
+      const long long a = p->pre[t], z = p->pre[t + 1];
+      if (a >= e) return false;
+      if (z == a || z <= s) {  // no cached token, or before the range
+        ++t;
+        continue;
+      }
+      const int4 info = p->tiles[t];
+      const long long lo = s > a ? s : a, hi = e < z ? e : z;
+      g.row0 = info.x;
+      g.rows = info.y;
+      g.b = info.z;
+      g.len = info.w;
+      g.blk_lo = static_cast<int>(lo - a);
+      g.blk_hi = static_cast<int>(hi - a);
+      g.slot = lo == a && hi == z ? -1 : 2 * engine + (count == 0 ? 0 : 1);
+      ++count;
+      ++t;
+      return true;
+    }
+    return false;
+  }
+};
+
+struct Ctx {
+  const ChunkParams* p;
+  uint32_t base;
+  uint8_t* gbase;
+  Barriers* bars;
+  uint32_t tmem;
+  WaitCtx wc;
+  int engine, rank, warp, lane;
+};
+
+__device__ __forceinline__ uint32_t bar_addr(const uint64_t& b) { return smem_u32(&b); }
+
+struct BlockCursor {
+  const int32_t* row;
+  int nblk, base, cached;
+  __device__ void reset(const ChunkParams& p, const Seg& g) {
+    row = p.block_table + size_t(g.b) * p.max_blocks;
+    nblk = nblocks_of(g.len);
+    base = -64;
+    cached = -1;
+  }
+  __device__ int id(int j, int lane) {
+    if (j < base || j >= base + 32) {
+      base = j;
+      cached = (j + lane < nblk) ? row[j + lane] : -1;
+    }
+    return __shfl_sync(0xffffffffu, cached, j - base);
+  }
+};
+
+// Valid rows of block j (0 for a bad id); *blk receives a block that is safe to load.
+__device__ __forceinline__ int block_rows(const ChunkParams& p, const Seg& g, BlockCursor& cur, int j, int lane,
+                                          int* blk) {
+  const int id = cur.id(j, lane);
+  const bool ok = id >= 0 && id < p.num_blocks;
+  *blk = ok ? id : 0;
+  const int nv = min(g.len - j * kBlock, kBlock);
+  return ok ? nv : 0;
+}
+
+// Blocks of a pass that each CTA of the score pair loads: with up to two
+// blocks one each (N = 128), else two each (N = 256); block k of the pass is
+// S columns 64k..64k+63 either way.
+__device__ __forceinline__ int blocks_per_cta(int nb) { return nb > 2 ? 2 : 1; }
+
+// ------------------------------------------------------------------ score pair
+
+__device__ void score_tma_k(const Ctx& c, const CUtensorMap* kmap) {
+  const ChunkParams& p = *c.p;
+  Walker w;
+  w.init(p, c.engine);
+  Seg g;
+  BlockCursor cur;
+  uint32_t fit = 0;
+  const uint32_t full0 = map_to_rank(bar_addr(c.bars->k_full[0]), 0);
+  if (c.lane == 0) prefetch_tmap(kmap);
+  while (w.next(g)) {
+    cur.reset(p, g);
+    for (int j = g.blk_lo; j < g.blk_hi; j += kPassBlocks) {
+      const int nb = min(kPassBlocks, g.blk_hi - j);
+      const int per = blocks_per_cta(nb);
+      int blk[2] = {0, 0};
+      int mine = 0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int kb = c.rank * per + k;
+        // every lane takes part in the cursor's shuffle
+        const int nv = block_rows(p, g, cur, kb < nb ? j + kb : j, c.lane, &blk[k]);
+        if (k < per && kb < nb) {
+          mine = k + 1;
+          if (nv == 0 && c.lane == 0) atomicOr(p.err, kErrBadBlock);
+        }
+      }
+      for (int ch = 0; ch < kChunks; ++ch, ++fit) {
+        const int s = fit % kKSlots;
+        if (!warp_wait(bar_addr(c.bars->k_empty[s]), ((fit / kKSlots) & 1u) ^ 1u, c.wc)) return;
+        if (c.lane == 0) {
+          const uint32_t full = full0 + 8 * s;
+          mbar_arrive_expect_tx_remote(bar_addr(c.bars->k_full[s]), 0, static_cast<uint32_t>(mine) * kBlkChunk);
+          const uint32_t dst = c.base + k_slot_off(s);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (k < mine) pair_tma_load_2d(dst + k * kBlkChunk, kmap, 64 * ch, blk[k] * kBlock, full);
+        }
+        __syncwarp();
+      }
+    }
+  }
+}
+
+__device__ void score_tma_q(const Ctx& c, const CUtensorMap* qmap) {
+  const ChunkParams& p = *c.p;
+  Walker w;
+  w.init(p, c.engine);
+  Seg g;
+  uint32_t seg = 0;
+  const uint32_t full0 = map_to_rank(bar_addr(c.bars->q_full[0]), 0);
+  if (c.lane == 0) prefetch_tmap(qmap);
+  while (w.next(g)) {
+    for (int ch = 0; ch < kChunks; ++ch) {
+      if (!warp_wait(bar_addr(c.bars->q_empty[ch]), (seg & 1u) ^ 1u, c.wc)) return;
+      if (c.lane == 0) {
+        mbar_arrive_expect_tx_remote(bar_addr(c.bars->q_full[ch]), 0, kQChunk);
+        // rows past the tile belong to other tokens (or read as zeros): their
+        // scores are masked
+        pair_tma_load_2d(c.base + q_off(ch), qmap, 64 * ch, g.row0 + 128 * c.rank, full0 + 8 * ch);
+      }
+      __syncwarp();
+    }
+    ++seg;
+  }
+}
+
+// One thread of rank 0.
+__device__ bool score_mma_segment(const Ctx& c, const Seg& g, uint32_t seg, uint32_t& fit, uint32_t& pit) {
+  Barriers* bars = c.bars;
+  for (int j = g.blk_lo; j < g.blk_hi; j += kPassBlocks, ++pit) {
+    const bool first = j == g.blk_lo, last = j + kPassBlocks >= g.blk_hi;
+    const uint32_t idesc = idesc_qk(blocks_per_cta(min(kPassBlocks, g.blk_hi - j)));
+    const uint32_t d = c.tmem + 256 * (pit & 1u);
+    if (!wait_phase(bar_addr(bars->s_empty[pit & 1u]), ((pit >> 1) & 1u) ^ 1u, c.wc)) return false;
+    tc_fence_after();
+    for (int ch = 0; ch < kChunks; ++ch, ++fit) {
+      const int s = fit % kKSlots;
+      if (first && !wait_phase(bar_addr(bars->q_full[ch]), seg & 1u, c.wc)) return false;
+      if (!wait_phase(bar_addr(bars->k_full[s]), (fit / kKSlots) & 1u, c.wc)) return false;
+      const uint32_t qa = c.base + q_off(ch), ka = c.base + k_slot_off(s);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        pair_mma_ss(d, sw128_desc(qa + kk * 32, 16, 1024), sw128_desc(ka + kk * 32, 16, 1024), idesc,
+                    (ch | kk) ? 1u : 0u);
+      pair_commit(bar_addr(bars->k_empty[s]), kScoreMask);
+      if (last) pair_commit(bar_addr(bars->q_empty[ch]), kScoreMask);
+    }
+    pair_commit(bar_addr(bars->s_full[pit & 1u]), kScoreMask);
+  }
+  return true;
+}
+
+__device__ void score_mma(const Ctx& c) {
+  Walker w;
+  w.init(*c.p, c.engine);
+  Seg g;
+  uint32_t fit = 0, pit = 0, seg = 0;
+  while (w.next(g)) {
+    int ok = 1;
+    if (c.lane == 0) ok = score_mma_segment(c, g, seg, fit, pit) ? 1 : 0;
+    if (!__shfl_sync(0xffffffffu, ok, 0)) return;
+    ++seg;
+  }
+}
+
+// Swap a float with the other softmax thread of the same row.
+__device__ __forceinline__ bool xchg(const Ctx& c, int q4, int half, int h, uint32_t& xit, float mine, float* other) {
+  float* buf = reinterpret_cast<float*>(c.gbase + kXchgOff) + (xit & 1u) * 256;
+  buf[half * 128 + h] = mine;
+  mbar_arrive(bar_addr(c.bars->xchg[q4]));
+  if (!warp_wait(bar_addr(c.bars->xchg[q4]), xit & 1u, c.wc)) return false;
+  *other = buf[(half ^ 1) * 128 + h];
+  ++xit;
+  return true;
+}
+
+__device__ void score_softmax(const Ctx& c) {
+  const ChunkParams& p = *c.p;
+  const int q4 = c.warp & 3;           // TMEM lane quadrant
+  const int half = (c.warp - 4) >> 2;  // blocks half, half + 2 of each pass
+  const int h = q4 * 32 + c.lane;      // row of this CTA
+  const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+  // a zero scale (uniform attention) runs as a tiny one, so that a masked
+  // score (-inf) still gives exactly 0
+  const float sl2 = p.softmax_scale != 0.f ? p.softmax_scale * kLog2e : 1e-30f;
+  const bool pos = sl2 >= 0.f;
+  const float sg = pos ? 1.f : -1.f;
+  const uint32_t to = static_cast<uint32_t>(c.rank) + 2;
+  const uint32_t rec0 = map_to_rank(c.base + rec_off(0), to);
+  const uint32_t pfull0 = map_to_rank(bar_addr(c.bars->p_full[0]), to);
+  Walker w;
+  w.init(p, c.engine);
+  Seg g;
+  BlockCursor cur;
+  uint32_t it = 0, pit = 0, xit = 0;
+  bool alive = true;
+  while (alive && w.next(g)) {
+    cur.reset(p, g);
+    // this row's query token sees the tile's length without its last
+    // tokens' rows; padding rows see nothing
+    const int row = 128 * c.rank + h;
+    const int row_len = row < g.rows ? g.len - (g.rows - 1 - row) / p.H : 0;
+    float m_ref = -INFINITY, l = 0.f;
+    for (int j0 = g.blk_lo; j0 < g.blk_hi; j0 += kPassBlocks, ++pit) {
+      const bool first_pass = (j0 == g.blk_lo);
+      const int nb = min(kPassBlocks, g.blk_hi - j0);
+      int nvr[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int kb = half + 2 * k;
+        int blk;
+        const int nv = block_rows(p, g, cur, kb < nb ? j0 + kb : j0, c.lane, &blk);
+        nvr[k] = kb < nb ? max(0, min(nv, row_len - (j0 + kb) * kBlock)) : 0;
+      }
+      const uint32_t buf = pit & 1u;
+      if (!warp_wait(bar_addr(c.bars->s_full[buf]), (pit >> 1) & 1u, c.wc)) {
+        alive = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t sv[128];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        tmem_ld32(c.tmem + lane_off + 256 * buf + 64 * half + 128 * (q >> 1) + 32 * (q & 1),
+                  *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * q]));
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (c.lane == 0) mbar_arrive_remote(bar_addr(c.bars->s_empty[buf]), 0);
+
+      // masked columns take the score -sg * inf, which no max selects and
+      // whose exponential is exactly 0
+      if (!__all_sync(0xffffffffu, nvr[0] == kBlock && nvr[1] == kBlock)) {
+        const uint32_t masked = __float_as_uint(-INFINITY * sg);
+#pragma unroll
+        for (int t = 0; t < 128; ++t)
+          if ((t & 63) >= nvr[t >> 6]) sv[t] = masked;
+      }
+      float mr;
+      if (pos) {
+        float mv[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int t = 0; t < 128; t += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            mv[u] = fmax3(mv[u], __uint_as_float(sv[t + 2 * u]), __uint_as_float(sv[t + 2 * u + 1]));
+        mr = fmax3(fmaxf(mv[0], mv[1]), mv[2], mv[3]);
+      } else {
+        float mv[4] = {INFINITY, INFINITY, INFINITY, INFINITY};
+#pragma unroll
+        for (int t = 0; t < 128; t += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            mv[u] = fmin3(mv[u], __uint_as_float(sv[t + 2 * u]), __uint_as_float(sv[t + 2 * u + 1]));
+        mr = -fmin3(fminf(mv[0], mv[1]), mv[2], mv[3]);
+      }
+      const float mine = (nvr[0] | nvr[1]) ? mr * sg * sl2 : -INFINITY;
+      float other;
+      if (!xchg(c, q4, half, h, xit, mine, &other)) {
+        alive = false;
+        break;
+      }
+      const float mx = fmaxf(mine, other);
+      float alpha = 1.f;
+      bool resc = false;
+      if (first_pass) {
+        m_ref = mx;
+      } else if (mx > m_ref + kRescaleThreshold) {
+        alpha = (m_ref == -INFINITY) ? 0.f : ex2_approx(m_ref - mx);
+        m_ref = mx;
+        l *= alpha;
+        resc = true;
+      }
+      const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+      const unsigned any = __any_sync(0xffffffffu, resc);
+      const bool last_pass = j0 + kPassBlocks >= g.blk_hi;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int kb = half + 2 * k;
+        if (kb >= nb) continue;
+        const uint32_t ib = it + static_cast<uint32_t>(kb);
+        const int r = ib % kNP;
+        if (!warp_wait(bar_addr(c.bars->p_empty[r]), ((ib / kNP) & 1u) ^ 1u, c.wc)) {
+          alive = false;
+          break;
+        }
+        const uint32_t full = pfull0 + 8 * r;
+        const uint32_t rec = rec0 + r * kRecBytes;
+        // one arrival per warp announces its bytes: each lane's P row, for a
+        // pass's first block and the segment's last its factors, a flag
+        const bool meta = kb == 0 || (last_pass && kb == nb - 1);
+        if (c.lane == 0) mbar_arrive_expect_tx_cluster_relaxed(full, 32 * (128 + (meta ? 16 : 0)) + 4);
+        float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+        for (int tp = 0; tp < 4; ++tp) {
+          uint32_t pk[2][4];
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int t = 64 * k + 16 * tp + 8 * u + 2 * e;
+              const float e0 = ex2_approx(fmaf(__uint_as_float(sv[t]), sl2, neg_m));
+              const float e1 = ex2_approx(fmaf(__uint_as_float(sv[t + 1]), sl2, neg_m));
+              sum0 += e0;
+              sum1 += e1;
+              __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
+              pk[u][e] = *reinterpret_cast<uint32_t*>(&b2);
+            }
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            st_async_v4(rec + (2 * tp + u) * kPCoreK + h * 16, make_uint4(pk[u][0], pk[u][1], pk[u][2], pk[u][3]),
+                        full);
+        }
+        l += sum0 + sum1;
+        if (c.lane == 0) st_async_b32(rec + kPBytes + kMetaBytes + q4 * 4, (kb == 0 && any) ? 1u : 0u, full);
+        if (kb == 0 && !(last_pass && nb == 1))
+          st_async_v4(rec + kPBytes + h * 16,
+                      make_uint4(__float_as_uint(alpha), __float_as_uint(m_ref), __float_as_uint(l), 0u), full);
+      }
+      if (!alive) break;
+      float ltot = l;
+      if (last_pass) {
+        float lo;
+        if (!xchg(c, q4, half, h, xit, l, &lo)) {
+          alive = false;
+          break;
+        }
+        ltot = l + lo;
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int kb = half + 2 * k;
+        if (!(last_pass && kb == nb - 1)) continue;
+        const uint32_t ib = it + static_cast<uint32_t>(kb);
+        const int r = ib % kNP;
+        st_async_v4(rec0 + r * kRecBytes + kPBytes + h * 16,
+                    make_uint4(__float_as_uint(kb == 0 ? alpha : 1.f), __float_as_uint(m_ref), __float_as_uint(ltot),
+                               0u),
+                    pfull0 + 8 * r);
+      }
+      it += static_cast<uint32_t>(nb);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ value pair
+
+__device__ void value_tma(const Ctx& c, const CUtensorMap* kmap) {
+  const ChunkParams& p = *c.p;
+  Walker w;
+  w.init(p, c.engine);
+  Seg g;
+  BlockCursor cur;
+  uint32_t vit = 0;
+  const int col0 = 256 * (c.rank - 2);  // this CTA's half of the latent
+  if (c.lane == 0) prefetch_tmap(kmap);
+  while (w.next(g)) {
+    cur.reset(p, g);
+    for (int j = g.blk_lo; j < g.blk_hi; ++j, ++vit) {
+      int blk;
+      block_rows(p, g, cur, j, c.lane, &blk);
+      const int s = vit % kVSlots;
+      if (!warp_wait(bar_addr(c.bars->v_empty[s]), ((vit / kVSlots) & 1u) ^ 1u, c.wc)) return;
+      if (c.lane == 0) {
+        const uint32_t full = bar_addr(c.bars->v_full[s]);
+        mbar_arrive_expect_tx(full, kVSlot);
+        const uint32_t dst = c.base + v_slot_off(s);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tma_load_2d(dst + q * kBlkChunk, kmap, col0 + 64 * q, blk * kBlock, full);
+      }
+      __syncwarp();
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t two) {
+  if ((two & 0x7f80u) == 0x7f80u) two &= 0xffff0000u;
+  if ((two & 0x7f800000u) == 0x7f800000u) two &= 0x0000ffffu;
+  return two;
+}
+
+// Rows past the tile's length are zeroed, so that whatever the cache holds
+// there (even NaN) contributes exactly 0 * 0.  Rows that the tile's last
+// token sees and its first does not lose their infinities and NaN: a token
+// that sees such a row has NaN or infinite scores, hence NaN probabilities,
+// and gets its NaN from those, while one that does not see it (P = 0) must
+// not meet 0 * NaN.
+__device__ void value_fixup(const Ctx& c) {
+  const ChunkParams& p = *c.p;
+  Walker w;
+  w.init(p, c.engine);
+  Seg g;
+  BlockCursor cur;
+  uint32_t vit = 0;
+  while (w.next(g)) {
+    cur.reset(p, g);
+    const int all_see = g.len - (g.rows - 1) / p.H;  // tokens that every row of the tile sees
+    for (int j = g.blk_lo; j < g.blk_hi; ++j, ++vit) {
+      int blk;
+      const int nv = block_rows(p, g, cur, j, c.lane, &blk);
+      const int s = vit % kVSlots;
+      if (!warp_wait(bar_addr(c.bars->v_full[s]), (vit / kVSlots) & 1u, c.wc)) return;
+      const int from = max(0, min(nv, all_see - j * kBlock));
+      if (from < kBlock) {
+        uint8_t* st = c.gbase + v_slot_off(s);
+        const int rows = kBlock - from;
+        for (int idx = c.lane; idx < rows * 4 * 8; idx += 32) {
+          const int ch = idx / (rows * 8), rem = idx % (rows * 8);
+          const int row = from + rem / 8;
+          uint4* at = reinterpret_cast<uint4*>(st + ch * kBlkChunk + row * 128 + (rem % 8) * 16);
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (row < nv) {
+            v = *at;
+            v = make_uint4(finite_or_zero(v.x), finite_or_zero(v.y), finite_or_zero(v.z), finite_or_zero(v.w));
+          }
+          *at = v;
+        }
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (c.lane == 0) mbar_arrive_remote(bar_addr(c.bars->v_ready[s]), 2);
+    }
+  }
+}
+
+// Rank 3: tells rank 2's MMA thread that this CTA's P record landed, and
+// whether a row of it asks for a rescale.
+__device__ void value_relay(const Ctx& c) {
+  Walker w;
+  w.init(*c.p, c.engine);
+  Seg g;
+  uint32_t it = 0;
+  while (w.next(g)) {
+    int ok = 1;
+    if (c.lane == 0) {
+      for (int j = g.blk_lo; j < g.blk_hi; ++j, ++it) {
+        const int r = it % kNP;
+        if (!wait_phase(bar_addr(c.bars->p_full[r]), (it / kNP) & 1u, c.wc)) {
+          ok = 0;
+          break;
+        }
+        const uint32_t* flags = reinterpret_cast<const uint32_t*>(c.gbase + rec_off(r) + kPBytes + kMetaBytes);
+        const uint32_t any = flags[0] | flags[1] | flags[2] | flags[3];
+        fence_proxy_async_smem();
+        st_cluster_b32(map_to_rank(smem_u32(&c.bars->peer_flag[r]), 2), any);
+        mbar_arrive_remote(bar_addr(c.bars->p_peer[r]), 2);
+      }
+    }
+    if (!__shfl_sync(0xffffffffu, ok, 0)) return;
+  }
+}
+
+constexpr uint32_t kReqFinal = 0x80000000u;
+
+// Posts a request to the epilogue warps of both CTAs: the word, an arrival,
+// and a commit (the MMAs issued so far are done).
+__device__ __forceinline__ void post_request(const Ctx& c, uint32_t req) {
+  *reinterpret_cast<volatile uint32_t*>(&c.bars->req) = req;
+  st_cluster_b32(map_to_rank(smem_u32(&c.bars->req), 3), req);
+  mbar_arrive(bar_addr(c.bars->epi_req));
+  mbar_arrive_remote(bar_addr(c.bars->epi_req), 3);
+  pair_commit(bar_addr(c.bars->epi_req), kValueMask);
+}
+
+// One thread of rank 2.
+__device__ bool value_mma_segment(const Ctx& c, const Seg& g, uint32_t seg, uint32_t& it, uint32_t& ncorr) {
+  Barriers* bars = c.bars;
+  if (seg > 0) {
+    if (!wait_phase(bar_addr(bars->o_free), (seg - 1) & 1u, c.wc)) return false;
+    tc_fence_after();
+  }
+  for (int j = g.blk_lo; j < g.blk_hi; ++j, ++it) {
+    const int r = it % kNP, s = it % kVSlots;
+    const bool first = (j == g.blk_lo), last = (j == g.blk_hi - 1);
+    if (!wait_phase(bar_addr(bars->p_full[r]), (it / kNP) & 1u, c.wc)) return false;
+    if (!wait_phase(bar_addr(bars->p_peer[r]), (it / kNP) & 1u, c.wc)) return false;
+    const uint32_t* flags = reinterpret_cast<const uint32_t*>(c.gbase + rec_off(r) + kPBytes + kMetaBytes);
+    const uint32_t any = flags[0] | flags[1] | flags[2] | flags[3] |
+                         *reinterpret_cast<volatile uint32_t*>(&bars->peer_flag[r]);
+    if (any && !first) {
+      post_request(c, static_cast<uint32_t>(r));
+      if (!wait_phase(bar_addr(bars->corr_done), ncorr & 1u, c.wc)) return false;
+      ++ncorr;
+      tc_fence_after();
+    }
+    fence_proxy_async_smem();
+    if (!wait_phase(bar_addr(bars->v_ready[s]), (it / kVSlots) & 1u, c.wc)) return false;
+    const uint32_t pa = c.base + rec_off(r), va = c.base + v_slot_off(s);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int k = 0; k < kBlock / 16; ++k)
+        pair_mma_ss(c.tmem + 256 * n, plain_desc(pa + k * 2 * kPCoreK, kPCoreK, 128),
+                    sw128_desc(va + 2 * n * kBlkChunk + k * 2048, kBlkChunk, 1024), kIdescPV,
+                    (k > 0 || !first) ? 1u : 0u);
+    pair_commit(bar_addr(bars->v_empty[s]), kValueMask);
+    if (last)
+      post_request(c, kReqFinal | static_cast<uint32_t>(r));  // the epilogues release the record
+    else
+      pair_commit(bar_addr(bars->p_empty[r]), kScoreMask);
+  }
+  return true;
+}
+
+__device__ void value_mma(const Ctx& c) {
+  Walker w;
+  w.init(*c.p, c.engine);
+  Seg g;
+  uint32_t it = 0, seg = 0, ncorr = 0;
+  while (w.next(g)) {
+    int ok = 1;
+    if (c.lane == 0) ok = value_mma_segment(c, g, seg, it, ncorr) ? 1 : 0;
+    if (!__shfl_sync(0xffffffffu, ok, 0)) return;
+    ++seg;
+  }
+}
+
+// Latent column of TMEM column c: every MMA's N = 256 columns are 128 of each
+// CTA's half.
+__device__ __forceinline__ int latent_of(int c) { return 256 * ((c >> 7) & 1) + 128 * (c >> 8) + (c & 127); }
+
+// Thread = (row, half of the TMEM columns).
+__device__ void value_epilogue(const Ctx& c) {
+  const ChunkParams& p = *c.p;
+  const int q4 = c.warp & 3;
+  const int half = (c.warp - 4) >> 2;
+  const int h = q4 * 32 + c.lane;
+  const int row = 128 * (c.rank - 2) + h;
+  const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+  const uint32_t ocol = 256 * half;
+  Walker w;
+  w.init(p, c.engine);
+  Seg g;
+  uint32_t nreq = 0, nfinal = 0;
+  while (w.next(g)) {
+    for (;;) {
+      if (!warp_wait(bar_addr(c.bars->epi_req), nreq & 1u, c.wc)) return;
+      ++nreq;
+      tc_fence_after();
+      const uint32_t req = *reinterpret_cast<volatile uint32_t*>(&c.bars->req);
+      const uint8_t* rec = c.gbase + rec_off(static_cast<int>(req & 0xffu));
+      const float4 meta = *reinterpret_cast<const float4*>(rec + kPBytes + h * 16);
+      if (!(req & kReqFinal)) {
+        const float alpha = meta.x;
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+          for (int ch = 0; ch < 8; ++ch) {
+            uint32_t v[32];
+            tmem_ld32(c.tmem + lane_off + ocol + 32 * ch, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int t = 0; t < 32; ++t) v[t] = __float_as_uint(__uint_as_float(v[t]) * alpha);
+            tmem_st32(c.tmem + lane_off + ocol + 32 * ch, v);
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (c.lane == 0) mbar_arrive_remote(bar_addr(c.bars->corr_done), 2);
+        continue;
+      }
+      const float m_fin = meta.y, l_fin = meta.z;
+      __syncwarp();
+      if (c.lane == 0) mbar_arrive(bar_addr(c.bars->meta_done));
+      if (c.warp == 4) {
+        if (!warp_wait(bar_addr(c.bars->meta_done), nfinal & 1u, c.wc)) return;
+        if (c.lane == 0) mbar_arrive_remote(bar_addr(c.bars->p_empty[req & 0xffu]), c.rank - 2);
+      }
+      ++nfinal;
+      const bool live = row < g.rows;
+      const float inv = l_fin > 0.f ? 1.f / l_fin : (l_fin == 0.f ? 0.f : l_fin);  // a NaN sum stays NaN
+      const float lse = l_fin == 0.f ? -INFINITY : (m_fin + log2f(l_fin)) * 0.6931471805599453f;
+#pragma unroll 1
+      for (int ch = 0; ch < 8; ++ch) {
+        uint32_t v[32];
+        tmem_ld32(c.tmem + lane_off + ocol + 32 * ch, v);
+        tmem_ld_wait();
+        if (!live) continue;
+        const int col = latent_of(ocol + 32 * ch);
+        if (g.slot < 0) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + (size_t(g.row0) + row) * kDc + col);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t w4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[8 * q + 2 * e]) * inv,
+                                                        __uint_as_float(v[8 * q + 2 * e + 1]) * inv);
+              w4[e] = *reinterpret_cast<uint32_t*>(&b2);
+            }
+            dst[q] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+          }
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.o_part + (size_t(g.slot) * kTileRows + row) * kDc + col);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            dst[q] = make_float4(__uint_as_float(v[4 * q]) * inv, __uint_as_float(v[4 * q + 1]) * inv,
+                                 __uint_as_float(v[4 * q + 2]) * inv, __uint_as_float(v[4 * q + 3]) * inv);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (c.lane == 0) mbar_arrive_remote(bar_addr(c.bars->o_free), 2);
+      if (live && half == 0) {
+        if (g.slot < 0)
+          p.lse[size_t(g.row0) + row] = lse;
+        else
+          p.lse_part[size_t(g.slot) * kTileRows + row] = lse;
+      }
+      break;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ kernels
+
+__global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
+chunk_sm100_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap,
+                   const ChunkParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t base = smem_u32(smem_raw);
+  Barriers* bars = reinterpret_cast<Barriers*>(smem_raw);
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kKSlots; ++s) {
+      mbar_init(bar_addr(bars->k_full[s]), 2);     // both producers
+      mbar_init(bar_addr(bars->k_empty[s]), 1);
+    }
+    for (int ch = 0; ch < kChunks; ++ch) {
+      mbar_init(bar_addr(bars->q_full[ch]), 2);
+      mbar_init(bar_addr(bars->q_empty[ch]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar_addr(bars->s_full[s]), 1);
+      mbar_init(bar_addr(bars->s_empty[s]), 16);   // eight softmax warps of two CTAs
+    }
+    for (int q = 0; q < 4; ++q) mbar_init(bar_addr(bars->xchg[q]), 64);  // two warps
+    for (int r = 0; r < kNP; ++r) {
+      mbar_init(bar_addr(bars->p_empty[r]), 1);    // PV commit, or the epilogue (segment end)
+      mbar_init(bar_addr(bars->p_full[r]), 4);     // the four softmax warps of one half
+      mbar_init(bar_addr(bars->p_peer[r]), 1);
+    }
+    for (int s = 0; s < kVSlots; ++s) {
+      mbar_init(bar_addr(bars->v_full[s]), 1);
+      mbar_init(bar_addr(bars->v_ready[s]), 2);    // the fixup warps of two CTAs
+      mbar_init(bar_addr(bars->v_empty[s]), 1);
+    }
+    mbar_init(bar_addr(bars->epi_req), 2);         // request posted + commit
+    mbar_init(bar_addr(bars->corr_done), 16);
+    mbar_init(bar_addr(bars->o_free), 16);
+    mbar_init(bar_addr(bars->meta_done), 8);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    pair_tmem_alloc(smem_u32(&bars->tmem_base), kTmemCols);
+    pair_tmem_relinquish();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  // programmatic stream serialization: the set-up above overlaps the plan
+  // kernel; the merge kernel may be scheduled now (it waits for this grid)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  Ctx c;
+  c.p = &p;
+  c.base = base;
+  c.gbase = smem_raw;
+  c.bars = bars;
+  c.tmem = bars->tmem_base;
+  c.wc = WaitCtx{p.spin_limit, p.err, &bars->abort, p.err + 1};
+  c.engine = blockIdx.x >> 2;
+  c.rank = rank;
+  c.warp = warp;
+  c.lane = lane;
+
+  if ((base & 1023u) != 0) {
+    // swizzled tiles need 1024-byte aligned shared memory: nothing was
+    // issued, the call reads as one that gave up
+    if (threadIdx.x == 0) atomicOr(p.err, kErrTimeout);
+  } else if (rank < 2) {
+    if (warp == 0) score_tma_k(c, &kmap);
+    else if (warp == 1 && rank == 0) score_mma(c);
+    else if (warp == 2) score_tma_q(c, &qmap);
+    else if (warp >= 4) score_softmax(c);
+  } else {
+    if (warp == 0) value_tma(c, &kmap);
+    else if (warp == 1 && rank == 2) value_mma(c);
+    else if (warp == 2) value_fixup(c);
+    else if (warp == 3 && rank == 3) value_relay(c);
+    else if (warp >= 4) value_epilogue(c);
+  }
+
+  __syncthreads();
+  if (bars->abort) {
+    // let any asynchronous copy still in flight land before the CTA exits
+    if (threadIdx.x == 0) {
+      const long long t0 = clock64();
+      while (clock64() - t0 < 20000000LL) __nanosleep(1000);
+    }
+    __syncthreads();
+  }
+  // no CTA leaves (or frees TMEM) while another of its cluster may still
+  // signal it or run MMAs on its memory
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    pair_tmem_dealloc(c.tmem, kTmemCols);
+  }
+  cluster_sync();
+}
+
+constexpr int kPlanThreads = 1024;
+
+// Inclusive scan of one value per thread over the block.
+template <class T>
+__device__ T block_scan(T v, T* warp_sums, T* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  T w = warp_sums[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += u;
+  }
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  return v + (warp > 0 ? __shfl_sync(0xffffffffu, w, warp - 1) : T(0));
+}
+
+// The tile list: tiles of up to 256 / H tokens of one sequence, and the
+// running count of the cache blocks they read.
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ long long sums[32];
+  __shared__ int isums[32];
+  const int per = kTileRows / p.H;
+  int nt = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    const int b = b0 + threadIdx.x;
+    int tiles = 0;
+    if (b < p.B) {
+      const int a = p.q_offsets[b], e = p.q_offsets[b + 1];
+      checked_len(p.seq_lens, b, p.max_blocks, p.err);
+      if (a < 0 || e < a || e > p.T)
+        atomicOr(p.err, kErrSeqTooLong);
+      else
+        tiles = (e - a + per - 1) / per;
+    }
+    int total;
+    const int incl = block_scan(tiles, isums, &total);
+    // only offsets that decrease somewhere can ask for more tiles than T
+    // tokens fill: what is over is left out
+    if (b < p.B) {
+      p.tile_off[b] = min(p.max_tiles, nt + incl - tiles);
+      if (nt + incl > p.max_tiles) atomicOr(p.err, kErrSeqTooLong);
+    }
+    nt = min(p.max_tiles, nt + total);
+  }
+  if (threadIdx.x == 0) {
+    p.tile_off[p.B] = nt;
+    *p.n_tiles = nt;
+    p.pre[0] = 0;
+  }
+  __syncthreads();
+  long long blocks = 0;
+  for (int t0 = 0; t0 < nt; t0 += kPlanThreads) {
+    const int t = t0 + threadIdx.x;
+    long long mine = 0;
+    if (t < nt) {
+      int lo = 0, hi = p.B;  // tile_off[lo] <= t < tile_off[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.tile_off[mid] <= t) lo = mid; else hi = mid;
+      }
+      const int a = p.q_offsets[lo], n = p.q_offsets[lo + 1] - a;
+      const int j = (t - p.tile_off[lo]) * per;
+      const int tok = min(per, n - j);
+      // the tile's last token sees the sequence without the n - j - tok tokens behind it
+      const int len = max(0, checked_len(p.seq_lens, lo, p.max_blocks, nullptr) - (n - j - tok));
+      p.tiles[t] = make_int4((a + j) * p.H, tok * p.H, lo, len);
+      mine = nblocks_of(len);
+    }
+    long long total;
+    const long long incl = block_scan(mine, sums, &total);
+    if (t < nt) p.pre[t + 1] = blocks + incl;
+    blocks += total;
+  }
+}
+
+constexpr int kMergeRows = 8;  // one warp per row
+constexpr int kMergeThreads = 32 * kMergeRows;
+
+__device__ __forceinline__ void fill_row(const ChunkParams& p, size_t row, float lse, int lane) {
+  uint4* dst = reinterpret_cast<uint4*>(p.out + row * kDc + lane * 16);
+  dst[0] = make_uint4(0u, 0u, 0u, 0u);
+  dst[1] = make_uint4(0u, 0u, 0u, 0u);
+  if (lane == 0) p.lse[row] = lse;
+}
+
+// grid (engine boundaries, 256 / 8): the boundary at which a cut tile's first
+// piece ends merges that tile's rows:
+//   lse = M + log sum_i exp(lse_i - M),  out = sum_i exp(lse_i - lse) o_i.
+// Rows of tokens that see no cached token are written here, and after a
+// timeout every row of the call.
+__global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int wrow = blockIdx.y * kMergeRows + (threadIdx.x >> 5);  // 0..255
+  const int nt = *p.n_tiles;
+  if ((*reinterpret_cast<volatile uint32_t*>(p.err) & kErrTimeout) != 0) {
+    for (int t = blockIdx.x; t < nt; t += gridDim.x)
+      if (wrow < p.tiles[t].y) fill_row(p, size_t(p.tiles[t].x) + wrow, NAN, lane);
+    return;
+  }
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const int a = p.q_offsets[b], e = p.q_offsets[b + 1];
+    if (a < 0 || e < a || e > p.T) continue;
+    const int blind = e - a - checked_len(p.seq_lens, b, p.max_blocks, nullptr);  // tokens that see nothing
+    for (long long r = wrow; r < static_cast<long long>(blind) * p.H; r += kTileRows)
+      fill_row(p, size_t(a) * p.H + r, -INFINITY, lane);
+  }
+  const long long total = p.pre[nt];
+  const int P = total < p.P ? static_cast<int>(total) : p.P;
+  const int e1 = blockIdx.x + 1;  // the boundary between engines e1 - 1 and e1
+  if (e1 >= P) return;
+  const long long x = range_start(e1, total, P);
+  const int t = tile_of(p.pre, nt, x);
+  const long long a = p.pre[t], z = p.pre[t + 1];
+  const long long s0 = range_start(e1 - 1, total, P);
+  // merged at the boundary whose left engine holds the tile's first block
+  if (x == a || s0 > a) return;
+  const int4 info = p.tiles[t];
+  if (wrow >= info.y) return;
+  const int last = engine_of(z - 1, total, P);
+  const int n = last - (e1 - 1) + 1;
+  auto slot_of = [&](int i) { return 2 * (e1 - 1 + i) + (i == 0 && s0 != a ? 1 : 0); };
+  float M = -INFINITY;
+  for (int i = 0; i < n; ++i) {
+    const float v = p.lse_part[size_t(slot_of(i)) * kTileRows + wrow];
+    M = v != v ? v : fmaxf(M, v);
+    if (v != v) break;
+  }
+  const size_t row = size_t(info.x) + wrow;
+  if (M == -INFINITY) {
+    fill_row(p, row, -INFINITY, lane);
+    return;
+  }
+  float sum = 0.f;
+  for (int i = 0; i < n; ++i) sum += expf(p.lse_part[size_t(slot_of(i)) * kTileRows + wrow] - M);
+  const float L = M + logf(sum);
+  float acc[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+  for (int i = 0; i < n; ++i) {
+    const size_t r = size_t(slot_of(i)) * kTileRows + wrow;
+    const float li = p.lse_part[r];
+    if (li == -INFINITY) continue;
+    const float wgt = expf(li - L);
+    const float4* src = reinterpret_cast<const float4*>(p.o_part + r * kDc + lane * 16);
+    float4 v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = src[q];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      acc[4 * q] += wgt * v[q].x;
+      acc[4 * q + 1] += wgt * v[q].y;
+      acc[4 * q + 2] += wgt * v[q].z;
+      acc[4 * q + 3] += wgt * v[q].w;
+    }
+  }
+  uint32_t pk[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    __nv_bfloat162 b2 = __floats2bfloat162_rn(acc[2 * k], acc[2 * k + 1]);
+    pk[k] = *reinterpret_cast<uint32_t*>(&b2);
+  }
+  uint4* dst = reinterpret_cast<uint4*>(p.out + row * kDc + lane * 16);
+  dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+  dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+  if (lane == 0) p.lse[row] = L;
+}
+
+cudaError_t set_attributes() {
+  return cudaFuncSetAttribute(chunk_sm100_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes));
+}
+
+}  // namespace
+
+int chunk_sm100_max_clusters() {
+  if (set_attributes() != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(4);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, chunk_sm100_kernel, &cfg) != cudaSuccess) return 0;
+  return n;
+}
+
+cudaError_t launch_chunk_sm100(const ChunkParams& p, const CUtensorMap& kmap, const CUtensorMap& qmap,
+                               cudaStream_t stream) {
+  static std::atomic<bool> attr_set[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    if (cudaError_t e = set_attributes(); e != cudaSuccess) return e;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  chunk_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+  if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = stream;
+  cfg.gridDim = dim3(4 * p.P);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_sm100_kernel, kmap, qmap, p); e != cudaSuccess) return e;
+  cfg.gridDim = dim3(p.P, kTileRows / kMergeRows);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel, p);
+}
+
+}  // namespace mla

@@ -117,9 +117,22 @@ struct ChunkParams {
   float softmax_scale;
   __nv_bfloat16* out;  // [T,H,512]
   float* lse;          // [T,H]
+  int P;               // number of split-KV engines
+  int max_tiles;
+  long long spin_limit;
+  // workspace (chunk_layout in plan.h)
   uint32_t* err;
+  int* n_tiles;        // tiles in the list
+  int* tile_off;       // [B+1] first tile of each sequence
+  int4* tiles;         // [max_tiles] (first row of q, rows, sequence, cached tokens seen by the last query token)
+  long long* pre;      // [max_tiles+1] cache blocks of the tiles before each
+  float* lse_part;     // [2P][256]
+  float* o_part;       // [2P][256][512]
 };
-cudaError_t launch_chunk_simple(const ChunkParams& p, cudaStream_t stream);
+// Plan, attention and merge kernels.  kmap, qmap: as for launch_weigh.
+cudaError_t launch_chunk_sm100(const ChunkParams& p, const CUtensorMap& kmap, const CUtensorMap& qmap,
+                               cudaStream_t stream);
+int chunk_sm100_max_clusters();
 
 struct WeighParams {
   const __nv_bfloat16* q;    // [T,H,576]

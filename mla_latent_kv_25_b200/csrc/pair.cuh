@@ -1,0 +1,55 @@
+// Inline-PTX wrappers for pairs of CTAs (cta_group::2): the two CTAs of a
+// cluster whose ranks differ in the last bit run one MMA on both SMs, issued
+// by one thread of the even CTA.  A (M rows) and B (N rows) are split in
+// halves over the two CTAs' shared memory, at the same offsets in both; each
+// CTA's TMEM holds the accumulator rows of its half of M (M = 256: 128 lanes).
+// No multicast TMA loads.
+#pragma once
+
+#include "sm100.cuh"
+
+namespace mla {
+namespace sm100 {
+
+// One warp of each CTA of the pair calls these.
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void pair_tmem_relinquish() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// D[tmem of both] (+)= A * B, bf16 operands, fp32 accumulation.
+__device__ __forceinline__ void pair_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrive on the barrier at local offset `bar` in every CTA of `mask` once all
+// MMAs this thread issued have completed.
+__device__ __forceinline__ void pair_commit(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(mask)
+      : "memory");
+}
+
+// TMA load into this CTA whose bytes are counted on a barrier of either CTA of
+// the pair (`bar`: a cluster address from map_to_rank).
+__device__ __forceinline__ void pair_tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+}  // namespace sm100
+}  // namespace mla

@@ -64,6 +64,31 @@ inline Fp8Plan plan_fp8_groups(int B, int rows, int max_blocks, int P, size_t ws
   }
 }
 
+// A chunk call's tile: query rows that one engine attends at once, whole
+// tokens of one sequence.
+constexpr int kChunkTileRows = 256;
+
+// Workspace of a chunk call of T tokens, B sequences and H heads on P engines:
+// error word; tile count; tile list; fp32 pieces of cut tiles (at most two per
+// engine).  A sequence of n tokens has ceil(n / (256 / H)) tiles.
+struct ChunkLayout {
+  int max_tiles;
+  size_t n_tiles, tile_off, tiles, pre, lse_part, o_part, total;
+};
+
+inline ChunkLayout chunk_layout(int T, int B, int H, int P) {
+  ChunkLayout w;
+  w.max_tiles = T / (kChunkTileRows / H) + B;
+  w.n_tiles = 256;
+  w.tile_off = 512;
+  w.tiles = align256(w.tile_off + (size_t(B) + 1) * 4);
+  w.pre = align256(w.tiles + size_t(w.max_tiles) * 16);
+  w.lse_part = align256(w.pre + (size_t(w.max_tiles) + 1) * 8);
+  w.o_part = align256(w.lse_part + size_t(2 * P) * kChunkTileRows * 4);
+  w.total = align256(w.o_part + size_t(2 * P) * kChunkTileRows * kDc * 4);
+  return w;
+}
+
 // Workspace of an eviction: error word, moves per sequence, move lists (at
 // most half of a sequence's slots are free below its budget and filled from
 // behind it).

@@ -1,0 +1,226 @@
+"""Host model of the chunk kernel's barrier protocol (csrc/chunk_sm100.cu): the
+roles of the four CTAs of an engine as generators over mbarrier phases, run in
+random interleavings over many segment patterns and rescale flags.  As for the
+decode kernel's model, a test fails on a deadlock, on more arrivals than a
+barrier's count and on a waiter lapped by two phases; commits and TMA loads
+complete at once.  A change to the kernel's waits, arrivals, ring sizes or
+counts must be made here too."""
+import random
+
+import pytest
+
+from tests.test_pipeline_protocol import Bar, _passes, _patterns
+
+K_SLOTS, V_SLOTS, N_REC, CHUNKS = 5, 4, 5, 9
+
+
+def roles(segs, flags, counts):
+    B = {}
+
+    def bar(name, count):
+        B[name] = Bar(name, counts.get(name.rstrip("0123456789_"), count))
+
+    def at(name, rank):
+        return f"{name}_{rank}"
+
+    for s in range(K_SLOTS):
+        bar(f"k_full{s}", 2)
+        for r in (0, 1):
+            bar(at(f"k_empty{s}", r), 1)
+    for ch in range(CHUNKS):
+        bar(f"q_full{ch}", 2)
+        for r in (0, 1):
+            bar(at(f"q_empty{ch}", r), 1)
+    for s in range(2):
+        bar(f"s_empty{s}", 16)
+        for r in (0, 1):
+            bar(at(f"s_full{s}", r), 1)
+    for r in (0, 1):
+        bar(at("xchg", r), 2)
+    for i in range(N_REC):
+        for r in (0, 1):
+            bar(at(f"p_empty{i}", r), 1)
+        for r in (2, 3):
+            bar(at(f"p_full{i}", r), 4)
+        bar(f"p_peer{i}", 1)
+    for s in range(V_SLOTS):
+        for r in (2, 3):
+            bar(at(f"v_full{s}", r), 1)
+            bar(at(f"v_empty{s}", r), 1)
+        bar(f"v_ready{s}", 2)
+    for r in (2, 3):
+        bar(at("epi_req", r), 2)
+        bar(at("meta_done", r), 8)
+    bar("corr_done", 16)
+    bar("o_free", 16)
+
+    def score_k(rank):
+        fit = 0
+        for lo, hi in segs:
+            for _ in _passes(lo, hi):
+                for _ch in range(CHUNKS):
+                    s = fit % K_SLOTS
+                    yield at(f"k_empty{s}", rank), ((fit // K_SLOTS) & 1) ^ 1, fit // K_SLOTS - 1
+                    B[f"k_full{s}"].arrive()
+                    fit += 1
+
+    def score_q(rank):
+        for seg, _ in enumerate(segs):
+            for ch in range(CHUNKS):
+                yield at(f"q_empty{ch}", rank), (seg & 1) ^ 1, seg - 1
+                B[f"q_full{ch}"].arrive()
+
+    def score_mma():
+        fit = pit = 0
+        for seg, (lo, hi) in enumerate(segs):
+            for j, nb in _passes(lo, hi):
+                yield f"s_empty{pit & 1}", ((pit >> 1) & 1) ^ 1, (pit >> 1) - 1
+                for ch in range(CHUNKS):
+                    s = fit % K_SLOTS
+                    if j == lo:
+                        yield f"q_full{ch}", seg & 1, seg
+                    yield f"k_full{s}", (fit // K_SLOTS) & 1, fit // K_SLOTS
+                    for r in (0, 1):
+                        B[at(f"k_empty{s}", r)].arrive()
+                        if j + nb >= hi:
+                            B[at(f"q_empty{ch}", r)].arrive()
+                    fit += 1
+                for r in (0, 1):
+                    B[at(f"s_full{pit & 1}", r)].arrive()
+                pit += 1
+
+    def softmax(rank, half):
+        it = pit = xit = 0
+        for lo, hi in segs:
+            for j0, nb in _passes(lo, hi):
+                yield at(f"s_full{pit & 1}", rank), (pit >> 1) & 1, pit >> 1
+                B[f"s_empty{pit & 1}"].arrive(4)
+                pit += 1
+                B[at("xchg", rank)].arrive()
+                yield at("xchg", rank), xit & 1, xit
+                xit += 1
+                last = j0 + nb >= hi
+                final = None
+                for kb in (half, half + 2):
+                    if kb >= nb:
+                        continue
+                    ib = it + kb
+                    r = ib % N_REC
+                    yield at(f"p_empty{r}", rank), ((ib // N_REC) & 1) ^ 1, ib // N_REC - 1
+                    if last and kb == nb - 1:
+                        final = r
+                    else:
+                        B[at(f"p_full{r}", rank + 2)].arrive(4)
+                if last:
+                    B[at("xchg", rank)].arrive()
+                    yield at("xchg", rank), xit & 1, xit
+                    xit += 1
+                if final is not None:
+                    B[at(f"p_full{final}", rank + 2)].arrive(4)
+                it += nb
+
+    def blocks():
+        i = 0
+        for lo, hi in segs:
+            for j in range(lo, hi):
+                yield i, j == lo, j == hi - 1
+                i += 1
+
+    def value_tma(rank):
+        for i, _, _ in blocks():
+            s = i % V_SLOTS
+            yield at(f"v_empty{s}", rank), ((i // V_SLOTS) & 1) ^ 1, i // V_SLOTS - 1
+            B[at(f"v_full{s}", rank)].arrive()
+
+    def fixup(rank):
+        for i, _, _ in blocks():
+            s = i % V_SLOTS
+            yield at(f"v_full{s}", rank), (i // V_SLOTS) & 1, i // V_SLOTS
+            B[f"v_ready{s}"].arrive()
+
+    def relay():
+        for i, _, _ in blocks():
+            r = i % N_REC
+            yield at(f"p_full{r}", 3), (i // N_REC) & 1, i // N_REC
+            B[f"p_peer{r}"].arrive()
+
+    def value_mma():
+        ncorr = seg = 0
+        for i, first, last in blocks():
+            r, s = i % N_REC, i % V_SLOTS
+            if first and seg > 0:
+                yield "o_free", (seg - 1) & 1, seg - 1
+            yield at(f"p_full{r}", 2), (i // N_REC) & 1, i // N_REC
+            yield f"p_peer{r}", (i // N_REC) & 1, i // N_REC
+            if flags[i] and not first:
+                for c in (2, 3):
+                    B[at("epi_req", c)].arrive(2)
+                yield "corr_done", ncorr & 1, ncorr
+                ncorr += 1
+            yield f"v_ready{s}", (i // V_SLOTS) & 1, i // V_SLOTS
+            for c in (2, 3):
+                B[at(f"v_empty{s}", c)].arrive()
+                if last:
+                    B[at("epi_req", c)].arrive(2)
+                else:
+                    B[at(f"p_empty{r}", c - 2)].arrive()
+            if last:
+                seg += 1
+
+    def epilogue(rank):
+        nreq = nfinal = 0
+        for i, first, last in blocks():
+            r = i % N_REC
+            if flags[i] and not first:
+                yield at("epi_req", rank), nreq & 1, nreq
+                nreq += 1
+                B["corr_done"].arrive(8)
+            if last:
+                yield at("epi_req", rank), nreq & 1, nreq
+                nreq += 1
+                B[at("meta_done", rank)].arrive(8)
+                yield at("meta_done", rank), nfinal & 1, nfinal
+                nfinal += 1
+                B[at(f"p_empty{r}", rank - 2)].arrive()
+                B["o_free"].arrive(8)
+
+    procs = {"score_mma": score_mma(), "value_mma": value_mma(), "relay": relay()}
+    for r in (0, 1):
+        procs |= {f"k{r}": score_k(r), f"q{r}": score_q(r), f"soft{r}a": softmax(r, 0), f"soft{r}b": softmax(r, 1),
+                  f"v{r + 2}": value_tma(r + 2), f"fix{r + 2}": fixup(r + 2), f"epi{r + 2}": epilogue(r + 2)}
+    return B, procs
+
+
+def simulate(segs, seed, counts=()):
+    rng = random.Random(seed)
+    flags = [rng.random() < 0.3 for _ in range(sum(hi - lo for lo, hi in segs))]
+    B, procs = roles(segs, flags, dict(counts))
+    waiting = {}
+    for name in list(procs):
+        waiting[name] = next(procs[name], None)
+    alive = {n for n in procs if waiting[n] is not None}
+    while alive:
+        moved = False
+        for name in rng.sample(sorted(alive), len(alive)):
+            while name in alive and B[waiting[name][0]].passes(*waiting[name][1:]):
+                moved = True
+                waiting[name] = next(procs[name], None)
+                if waiting[name] is None:
+                    alive.discard(name)
+                if rng.random() < 0.3:
+                    break
+        if not moved:
+            return {n: waiting[n] for n in alive}
+    return True
+
+
+def test_protocol_finishes_in_every_interleaving():
+    for i, segs in enumerate(_patterns()):
+        for seed in range(8):
+            res = simulate(segs, 1000 * seed + i)
+            assert res is True, f"segments {segs}, seed {seed}: blocked {res}"
+
+
+@pytest.mark.parametrize("name,count", [("p_empty", 2), ("v_ready", 3), ("q_full", 3), ("s_empty", 17), ("corr_done", 17)])
+def test_model_finds_planted_counts(name, count):
+    assert all(simulate([(0, 40), (0, 9), (0, 30)], seed, {name: count}) is not True for seed in range(3))
