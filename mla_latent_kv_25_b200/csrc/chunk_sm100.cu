@@ -12,9 +12,8 @@
 //   memory and half of the pass's 256 tokens;   of the latent columns of each block;
 //   S is double-buffered in TMEM                O fills TMEM
 //   w0 TMA of K, w2 TMA of Q, w1 MMA (rank 0)   w0 TMA of V, w1 MMA (rank 2), w2 zeroes
-//   w4-11 softmax of the CTA's 128 rows,        V rows past the length, w3 (rank 3)
-//         P by st.async to CTA rank + 2         relays P's arrival to rank 2,
-//                                               w4-11 rescale, output
+//   w4-11 softmax of the CTA's 128 rows,        V rows past the length, w3 relays P's
+//         P by st.async to CTA rank + 2         arrival to rank 2, w4-11 rescale, output
 //
 // Bound: the tensor pipe, 2 * rows * tokens * (576 + 512) FLOPs.  Why this
 // shape: with 256 rows to a cached token a pair reads 576 bytes of K (512 of
@@ -85,11 +84,11 @@ struct Barriers {
   uint64_t v_ready[kVSlots];                   // leader: both CTAs' V landed and cleaned
   uint64_t v_empty[kVSlots];                   // commit to both
   uint64_t p_full[kNP];                        // this CTA's P record landed
-  uint64_t p_peer[kNP];                        // leader: the peer's record landed
+  uint64_t p_ready[kNP];                       // leader: both CTAs' records landed
   uint64_t epi_req;                            // both: request posted + MMAs done
   uint64_t corr_done, o_free;                  // leader: all epilogue warps of both
   uint64_t meta_done;                          // all epilogue warps read the final record
-  uint32_t peer_flag[kNP];                     // leader: the peer record's rescale flags
+  alignas(8) uint32_t flag[kNP][2];            // leader: a row of each CTA's record asks for a rescale
   uint32_t req;
   uint32_t tmem_base;
   int abort;
@@ -243,7 +242,9 @@ __device__ void score_tma_k(const Ctx& c, const CUtensorMap* kmap) {
       const int nb = min(kPassBlocks, g.blk_hi - j);
       const int per = blocks_per_cta(nb);
       int blk[2] = {0, 0};
-      int mine = 0;
+      // blocks this CTA loads: at least one (a masked copy of the pass's first
+      // block if none is its own), so that neither CTA's ring runs ahead
+      int mine = 1;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int kb = c.rank * per + k;
@@ -258,8 +259,10 @@ __device__ void score_tma_k(const Ctx& c, const CUtensorMap* kmap) {
         const int s = fit % kKSlots;
         if (!warp_wait(bar_addr(c.bars->k_empty[s]), ((fit / kKSlots) & 1u) ^ 1u, c.wc)) return;
         if (c.lane == 0) {
+          // rank 0 announces the bytes of both CTAs; those of rank 1 may land first
           const uint32_t full = full0 + 8 * s;
-          mbar_arrive_expect_tx_remote(bar_addr(c.bars->k_full[s]), 0, static_cast<uint32_t>(mine) * kBlkChunk);
+          if (c.rank == 0)
+            mbar_arrive_expect_tx(bar_addr(c.bars->k_full[s]), static_cast<uint32_t>(max(nb, 2)) * kBlkChunk);
           const uint32_t dst = c.base + k_slot_off(s);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
@@ -283,7 +286,7 @@ __device__ void score_tma_q(const Ctx& c, const CUtensorMap* qmap) {
     for (int ch = 0; ch < kChunks; ++ch) {
       if (!warp_wait(bar_addr(c.bars->q_empty[ch]), (seg & 1u) ^ 1u, c.wc)) return;
       if (c.lane == 0) {
-        mbar_arrive_expect_tx_remote(bar_addr(c.bars->q_full[ch]), 0, kQChunk);
+        if (c.rank == 0) mbar_arrive_expect_tx(bar_addr(c.bars->q_full[ch]), 2 * kQChunk);
         // rows past the tile belong to other tokens (or read as zeros): their
         // scores are masked
         pair_tma_load_2d(c.base + q_off(ch), qmap, 64 * ch, g.row0 + 128 * c.rank, full0 + 8 * ch);
@@ -294,9 +297,17 @@ __device__ void score_tma_q(const Ctx& c, const CUtensorMap* qmap) {
   }
 }
 
-// One thread of rank 0.
+// One thread of rank 0.  The barrier of the next chunk is probed before the
+// current chunk's MMAs are issued: a probe behind them would wait for their
+// issue and leave the pipe idle meanwhile.
 __device__ bool score_mma_segment(const Ctx& c, const Seg& g, uint32_t seg, uint32_t& fit, uint32_t& pit) {
   Barriers* bars = c.bars;
+  const uint32_t fills = static_cast<uint32_t>((g.blk_hi - g.blk_lo + kPassBlocks - 1) / kPassBlocks) * kChunks;
+  const uint32_t end = fit + fills;
+  auto probe = [&](uint32_t f) {
+    return f < end && mbar_test_wait(bar_addr(bars->k_full[f % kKSlots]), (f / kKSlots) & 1u);
+  };
+  bool ready = probe(fit);
   for (int j = g.blk_lo; j < g.blk_hi; j += kPassBlocks, ++pit) {
     const bool first = j == g.blk_lo, last = j + kPassBlocks >= g.blk_hi;
     const uint32_t idesc = idesc_qk(blocks_per_cta(min(kPassBlocks, g.blk_hi - j)));
@@ -306,7 +317,8 @@ __device__ bool score_mma_segment(const Ctx& c, const Seg& g, uint32_t seg, uint
     for (int ch = 0; ch < kChunks; ++ch, ++fit) {
       const int s = fit % kKSlots;
       if (first && !wait_phase(bar_addr(bars->q_full[ch]), seg & 1u, c.wc)) return false;
-      if (!wait_phase(bar_addr(bars->k_full[s]), (fit / kKSlots) & 1u, c.wc)) return false;
+      if (!ready && !wait_phase(bar_addr(bars->k_full[s]), (fit / kKSlots) & 1u, c.wc)) return false;
+      ready = probe(fit + 1);
       const uint32_t qa = c.base + q_off(ch), ka = c.base + k_slot_off(s);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
@@ -358,6 +370,7 @@ __device__ void score_softmax(const Ctx& c) {
   const uint32_t to = static_cast<uint32_t>(c.rank) + 2;
   const uint32_t rec0 = map_to_rank(c.base + rec_off(0), to);
   const uint32_t pfull0 = map_to_rank(bar_addr(c.bars->p_full[0]), to);
+  const uint32_t sempty0 = map_to_rank(bar_addr(c.bars->s_empty[0]), 0);
   Walker w;
   w.init(p, c.engine);
   Seg g;
@@ -396,7 +409,7 @@ __device__ void score_softmax(const Ctx& c) {
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (c.lane == 0) mbar_arrive_remote(bar_addr(c.bars->s_empty[buf]), 0);
+      if (c.lane == 0) mbar_arrive_cluster_relaxed(sempty0 + 8 * buf);  // the loads are in registers
 
       // masked columns take the score -sg * inf, which no max selects and
       // whose exponential is exactly 0
@@ -562,6 +575,7 @@ __device__ void value_fixup(const Ctx& c) {
   Seg g;
   BlockCursor cur;
   uint32_t vit = 0;
+  const uint32_t ready0 = map_to_rank(bar_addr(c.bars->v_ready[0]), 2);
   while (w.next(g)) {
     cur.reset(p, g);
     const int all_see = g.len - (g.rows - 1) / p.H;  // tokens that every row of the tile sees
@@ -588,18 +602,27 @@ __device__ void value_fixup(const Ctx& c) {
         fence_proxy_async_smem();
       }
       __syncwarp();
-      if (c.lane == 0) mbar_arrive_remote(bar_addr(c.bars->v_ready[s]), 2);
+      if (c.lane == 0) {
+        if (from < kBlock)
+          mbar_arrive_remote(bar_addr(c.bars->v_ready[s]), 2);
+        else
+          mbar_arrive_cluster_relaxed(ready0 + 8 * s);
+      }
     }
   }
 }
 
-// Rank 3: tells rank 2's MMA thread that this CTA's P record landed, and
-// whether a row of it asks for a rescale.
+// Each value CTA tells rank 2's MMA thread that its P record landed, and
+// whether a row of it asks for a rescale.  P was written by asynchronous
+// stores of the score CTA: the proxy fence here makes it visible to the MMAs,
+// off the issuing thread's path.
 __device__ void value_relay(const Ctx& c) {
   Walker w;
   w.init(*c.p, c.engine);
   Seg g;
   uint32_t it = 0;
+  const uint32_t ready0 = map_to_rank(bar_addr(c.bars->p_ready[0]), 2);
+  const uint32_t flag0 = map_to_rank(smem_u32(&c.bars->flag[0][c.rank - 2]), 2);
   while (w.next(g)) {
     int ok = 1;
     if (c.lane == 0) {
@@ -609,11 +632,10 @@ __device__ void value_relay(const Ctx& c) {
           ok = 0;
           break;
         }
-        const uint32_t* flags = reinterpret_cast<const uint32_t*>(c.gbase + rec_off(r) + kPBytes + kMetaBytes);
-        const uint32_t any = flags[0] | flags[1] | flags[2] | flags[3];
+        const uint4 f = *reinterpret_cast<const uint4*>(c.gbase + rec_off(r) + kPBytes + kMetaBytes);
         fence_proxy_async_smem();
-        st_cluster_b32(map_to_rank(smem_u32(&c.bars->peer_flag[r]), 2), any);
-        mbar_arrive_remote(bar_addr(c.bars->p_peer[r]), 2);
+        mbar_arrive_expect_tx_cluster_relaxed(ready0 + 8 * r, 4);
+        st_async_b32(flag0 + 8 * r, f.x | f.y | f.z | f.w, ready0 + 8 * r);
       }
     }
     if (!__shfl_sync(0xffffffffu, ok, 0)) return;
@@ -632,29 +654,31 @@ __device__ __forceinline__ void post_request(const Ctx& c, uint32_t req) {
   pair_commit(bar_addr(c.bars->epi_req), kValueMask);
 }
 
-// One thread of rank 2.
+// One thread of rank 2; the next block's barriers are probed before the
+// current block's MMAs are issued.
 __device__ bool value_mma_segment(const Ctx& c, const Seg& g, uint32_t seg, uint32_t& it, uint32_t& ncorr) {
   Barriers* bars = c.bars;
   if (seg > 0) {
     if (!wait_phase(bar_addr(bars->o_free), (seg - 1) & 1u, c.wc)) return false;
     tc_fence_after();
   }
+  bool p_ok = false, v_ok = false;
   for (int j = g.blk_lo; j < g.blk_hi; ++j, ++it) {
     const int r = it % kNP, s = it % kVSlots;
     const bool first = (j == g.blk_lo), last = (j == g.blk_hi - 1);
-    if (!wait_phase(bar_addr(bars->p_full[r]), (it / kNP) & 1u, c.wc)) return false;
-    if (!wait_phase(bar_addr(bars->p_peer[r]), (it / kNP) & 1u, c.wc)) return false;
-    const uint32_t* flags = reinterpret_cast<const uint32_t*>(c.gbase + rec_off(r) + kPBytes + kMetaBytes);
-    const uint32_t any = flags[0] | flags[1] | flags[2] | flags[3] |
-                         *reinterpret_cast<volatile uint32_t*>(&bars->peer_flag[r]);
-    if (any && !first) {
+    if (!p_ok && !wait_phase(bar_addr(bars->p_ready[r]), (it / kNP) & 1u, c.wc)) return false;
+    const uint2 flags = make_uint2(*reinterpret_cast<volatile uint32_t*>(&bars->flag[r][0]),
+                                   *reinterpret_cast<volatile uint32_t*>(&bars->flag[r][1]));
+    if ((flags.x | flags.y) && !first) {
       post_request(c, static_cast<uint32_t>(r));
       if (!wait_phase(bar_addr(bars->corr_done), ncorr & 1u, c.wc)) return false;
       ++ncorr;
       tc_fence_after();
     }
-    fence_proxy_async_smem();
-    if (!wait_phase(bar_addr(bars->v_ready[s]), (it / kVSlots) & 1u, c.wc)) return false;
+    if (!v_ok && !wait_phase(bar_addr(bars->v_ready[s]), (it / kVSlots) & 1u, c.wc)) return false;
+    const uint32_t nx = it + 1;
+    p_ok = !last && mbar_test_wait(bar_addr(bars->p_ready[nx % kNP]), (nx / kNP) & 1u);
+    v_ok = !last && mbar_test_wait(bar_addr(bars->v_ready[nx % kVSlots]), (nx / kVSlots) & 1u);
     const uint32_t pa = c.base + rec_off(r), va = c.base + v_slot_off(s);
 #pragma unroll
     for (int n = 0; n < 2; ++n)
@@ -795,11 +819,11 @@ chunk_sm100_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kKSlots; ++s) {
-      mbar_init(bar_addr(bars->k_full[s]), 2);     // both producers
+      mbar_init(bar_addr(bars->k_full[s]), 1);
       mbar_init(bar_addr(bars->k_empty[s]), 1);
     }
     for (int ch = 0; ch < kChunks; ++ch) {
-      mbar_init(bar_addr(bars->q_full[ch]), 2);
+      mbar_init(bar_addr(bars->q_full[ch]), 1);
       mbar_init(bar_addr(bars->q_empty[ch]), 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -810,7 +834,7 @@ chunk_sm100_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     for (int r = 0; r < kNP; ++r) {
       mbar_init(bar_addr(bars->p_empty[r]), 1);    // PV commit, or the epilogue (segment end)
       mbar_init(bar_addr(bars->p_full[r]), 4);     // the four softmax warps of one half
-      mbar_init(bar_addr(bars->p_peer[r]), 1);
+      mbar_init(bar_addr(bars->p_ready[r]), 2);    // the relays of two CTAs
     }
     for (int s = 0; s < kVSlots; ++s) {
       mbar_init(bar_addr(bars->v_full[s]), 1);
@@ -861,7 +885,7 @@ chunk_sm100_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     if (warp == 0) value_tma(c, &kmap);
     else if (warp == 1 && rank == 2) value_mma(c);
     else if (warp == 2) value_fixup(c);
-    else if (warp == 3 && rank == 3) value_relay(c);
+    else if (warp == 3) value_relay(c);
     else if (warp >= 4) value_epilogue(c);
   }
 

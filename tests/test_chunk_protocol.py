@@ -24,7 +24,7 @@ def roles(segs, flags, counts):
         return f"{name}_{rank}"
 
     for s in range(K_SLOTS):
-        bar(f"k_full{s}", 2)
+        bar(f"k_full{s}", 2)                         # rank 0's arrival with its bytes, rank 1's bytes
         for r in (0, 1):
             bar(at(f"k_empty{s}", r), 1)
     for ch in range(CHUNKS):
@@ -42,7 +42,7 @@ def roles(segs, flags, counts):
             bar(at(f"p_empty{i}", r), 1)
         for r in (2, 3):
             bar(at(f"p_full{i}", r), 4)
-        bar(f"p_peer{i}", 1)
+        bar(f"p_ready{i}", 2)
     for s in range(V_SLOTS):
         for r in (2, 3):
             bar(at(f"v_full{s}", r), 1)
@@ -138,11 +138,11 @@ def roles(segs, flags, counts):
             yield at(f"v_full{s}", rank), (i // V_SLOTS) & 1, i // V_SLOTS
             B[f"v_ready{s}"].arrive()
 
-    def relay():
+    def relay(rank):
         for i, _, _ in blocks():
             r = i % N_REC
-            yield at(f"p_full{r}", 3), (i // N_REC) & 1, i // N_REC
-            B[f"p_peer{r}"].arrive()
+            yield at(f"p_full{r}", rank), (i // N_REC) & 1, i // N_REC
+            B[f"p_ready{r}"].arrive()
 
     def value_mma():
         ncorr = seg = 0
@@ -150,8 +150,7 @@ def roles(segs, flags, counts):
             r, s = i % N_REC, i % V_SLOTS
             if first and seg > 0:
                 yield "o_free", (seg - 1) & 1, seg - 1
-            yield at(f"p_full{r}", 2), (i // N_REC) & 1, i // N_REC
-            yield f"p_peer{r}", (i // N_REC) & 1, i // N_REC
+            yield f"p_ready{r}", (i // N_REC) & 1, i // N_REC
             if flags[i] and not first:
                 for c in (2, 3):
                     B[at("epi_req", c)].arrive(2)
@@ -184,10 +183,10 @@ def roles(segs, flags, counts):
                 B[at(f"p_empty{r}", rank - 2)].arrive()
                 B["o_free"].arrive(8)
 
-    procs = {"score_mma": score_mma(), "value_mma": value_mma(), "relay": relay()}
+    procs = {"score_mma": score_mma(), "value_mma": value_mma()}
     for r in (0, 1):
         procs |= {f"k{r}": score_k(r), f"q{r}": score_q(r), f"soft{r}a": softmax(r, 0), f"soft{r}b": softmax(r, 1),
-                  f"v{r + 2}": value_tma(r + 2), f"fix{r + 2}": fixup(r + 2), f"epi{r + 2}": epilogue(r + 2)}
+                  f"v{r + 2}": value_tma(r + 2), f"relay{r + 2}": relay(r + 2), f"fix{r + 2}": fixup(r + 2), f"epi{r + 2}": epilogue(r + 2)}
     return B, procs
 
 
