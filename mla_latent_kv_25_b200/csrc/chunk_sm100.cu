@@ -297,35 +297,37 @@ __device__ void score_tma_q(const Ctx& c, const CUtensorMap* qmap) {
   }
 }
 
-// One thread of rank 0.  The barrier of the next chunk is probed before the
-// current chunk's MMAs are issued: a probe behind them would wait for their
-// issue and leave the pipe idle meanwhile.
-__device__ bool score_mma_segment(const Ctx& c, const Seg& g, uint32_t seg, uint32_t& fit, uint32_t& pit) {
+// The elected thread of rank 0.  The barrier of the next chunk is probed
+// before the current chunk's MMAs are issued: a probe behind them would wait
+// for their issue and leave the pipe idle meanwhile.
+__device__ bool score_mma_segment(const Ctx& c, const Seg& g, uint32_t seg, uint32_t& slot, uint32_t& phase,
+                                  uint32_t& pit) {
   Barriers* bars = c.bars;
-  const uint32_t fills = static_cast<uint32_t>((g.blk_hi - g.blk_lo + kPassBlocks - 1) / kPassBlocks) * kChunks;
-  const uint32_t end = fit + fills;
-  auto probe = [&](uint32_t f) {
-    return f < end && mbar_test_wait(bar_addr(bars->k_full[f % kKSlots]), (f / kKSlots) & 1u);
-  };
-  bool ready = probe(fit);
+  const uint32_t k_full0 = bar_addr(bars->k_full[0]), k_empty0 = bar_addr(bars->k_empty[0]);
+  const uint32_t q_full0 = bar_addr(bars->q_full[0]), q_empty0 = bar_addr(bars->q_empty[0]);
+  const uint64_t q0 = sw128_desc(c.base + q_off(0), 16, 1024), k0 = sw128_desc(c.base + k_slot_off(0), 16, 1024);
+  bool ready = false;
   for (int j = g.blk_lo; j < g.blk_hi; j += kPassBlocks, ++pit) {
     const bool first = j == g.blk_lo, last = j + kPassBlocks >= g.blk_hi;
     const uint32_t idesc = idesc_qk(blocks_per_cta(min(kPassBlocks, g.blk_hi - j)));
     const uint32_t d = c.tmem + 256 * (pit & 1u);
     if (!wait_phase(bar_addr(bars->s_empty[pit & 1u]), ((pit >> 1) & 1u) ^ 1u, c.wc)) return false;
     tc_fence_after();
-    for (int ch = 0; ch < kChunks; ++ch, ++fit) {
-      const int s = fit % kKSlots;
-      if (first && !wait_phase(bar_addr(bars->q_full[ch]), seg & 1u, c.wc)) return false;
-      if (!ready && !wait_phase(bar_addr(bars->k_full[s]), (fit / kKSlots) & 1u, c.wc)) return false;
-      ready = probe(fit + 1);
-      const uint32_t qa = c.base + q_off(ch), ka = c.base + k_slot_off(s);
+#pragma unroll 1
+    for (int ch = 0; ch < kChunks; ++ch) {
+      if (first && !wait_phase(q_full0 + 8 * ch, seg & 1u, c.wc)) return false;
+      if (!ready && !wait_phase(k_full0 + 8 * slot, phase, c.wc)) return false;
+      const uint32_t s = slot;
+      if (++slot == kKSlots) {
+        slot = 0;
+        phase ^= 1u;
+      }
+      ready = mbar_test_wait(k_full0 + 8 * slot, phase);
+      const uint64_t qd = q0 + static_cast<uint32_t>(ch) * (kQChunk >> 4), kd = k0 + s * (kKSlot >> 4);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        pair_mma_ss(d, sw128_desc(qa + kk * 32, 16, 1024), sw128_desc(ka + kk * 32, 16, 1024), idesc,
-                    (ch | kk) ? 1u : 0u);
-      pair_commit(bar_addr(bars->k_empty[s]), kScoreMask);
-      if (last) pair_commit(bar_addr(bars->q_empty[ch]), kScoreMask);
+      for (int kk = 0; kk < 4; ++kk) pair_mma_ss(d, qd + 2 * kk, kd + 2 * kk, idesc, (ch | kk) ? 1u : 0u);
+      pair_commit(k_empty0 + 8 * s, kScoreMask);
+      if (last) pair_commit(q_empty0 + 8 * ch, kScoreMask);
     }
     pair_commit(bar_addr(bars->s_full[pit & 1u]), kScoreMask);
   }
@@ -333,16 +335,14 @@ __device__ bool score_mma_segment(const Ctx& c, const Seg& g, uint32_t seg, uint
 }
 
 __device__ void score_mma(const Ctx& c) {
-  Walker w;
-  w.init(*c.p, c.engine);
-  Seg g;
-  uint32_t fit = 0, pit = 0, seg = 0;
-  while (w.next(g)) {
-    int ok = 1;
-    if (c.lane == 0) ok = score_mma_segment(c, g, seg, fit, pit) ? 1 : 0;
-    if (!__shfl_sync(0xffffffffu, ok, 0)) return;
-    ++seg;
+  if (elect_one()) {
+    Walker w;
+    w.init(*c.p, c.engine);
+    Seg g;
+    uint32_t slot = 0, phase = 0, pit = 0, seg = 0;
+    while (w.next(g) && score_mma_segment(c, g, seg, slot, phase, pit)) ++seg;
   }
+  __syncwarp();
 }
 
 // Swap a float with the other softmax thread of the same row.
@@ -654,42 +654,43 @@ __device__ __forceinline__ void post_request(const Ctx& c, uint32_t req) {
   pair_commit(bar_addr(c.bars->epi_req), kValueMask);
 }
 
-// One thread of rank 2; the next block's barriers are probed before the
-// current block's MMAs are issued.
+// The elected thread of rank 2; the next block's barriers are probed before
+// the current block's MMAs are issued.
 __device__ bool value_mma_segment(const Ctx& c, const Seg& g, uint32_t seg, uint32_t& it, uint32_t& ncorr) {
   Barriers* bars = c.bars;
+  const uint64_t p0 = plain_desc(c.base + rec_off(0), kPCoreK, 128);
+  const uint64_t v0 = sw128_desc(c.base + v_slot_off(0), kBlkChunk, 1024);
   if (seg > 0) {
     if (!wait_phase(bar_addr(bars->o_free), (seg - 1) & 1u, c.wc)) return false;
     tc_fence_after();
   }
   bool p_ok = false, v_ok = false;
   for (int j = g.blk_lo; j < g.blk_hi; ++j, ++it) {
-    const int r = it % kNP, s = it % kVSlots;
+    const uint32_t r = it % kNP, s = it % kVSlots;
     const bool first = (j == g.blk_lo), last = (j == g.blk_hi - 1);
     if (!p_ok && !wait_phase(bar_addr(bars->p_ready[r]), (it / kNP) & 1u, c.wc)) return false;
-    const uint2 flags = make_uint2(*reinterpret_cast<volatile uint32_t*>(&bars->flag[r][0]),
-                                   *reinterpret_cast<volatile uint32_t*>(&bars->flag[r][1]));
-    if ((flags.x | flags.y) && !first) {
-      post_request(c, static_cast<uint32_t>(r));
+    const uint32_t flags = *reinterpret_cast<volatile uint32_t*>(&bars->flag[r][0]) |
+                           *reinterpret_cast<volatile uint32_t*>(&bars->flag[r][1]);
+    if (flags && !first) {
+      post_request(c, r);
       if (!wait_phase(bar_addr(bars->corr_done), ncorr & 1u, c.wc)) return false;
       ++ncorr;
       tc_fence_after();
     }
     if (!v_ok && !wait_phase(bar_addr(bars->v_ready[s]), (it / kVSlots) & 1u, c.wc)) return false;
     const uint32_t nx = it + 1;
-    p_ok = !last && mbar_test_wait(bar_addr(bars->p_ready[nx % kNP]), (nx / kNP) & 1u);
-    v_ok = !last && mbar_test_wait(bar_addr(bars->v_ready[nx % kVSlots]), (nx / kVSlots) & 1u);
-    const uint32_t pa = c.base + rec_off(r), va = c.base + v_slot_off(s);
+    p_ok = mbar_test_wait(bar_addr(bars->p_ready[nx % kNP]), (nx / kNP) & 1u);
+    v_ok = mbar_test_wait(bar_addr(bars->v_ready[nx % kVSlots]), (nx / kVSlots) & 1u);
+    const uint64_t pd = p0 + r * (kRecBytes >> 4), vd = v0 + s * (kVSlot >> 4);
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int k = 0; k < kBlock / 16; ++k)
-        pair_mma_ss(c.tmem + 256 * n, plain_desc(pa + k * 2 * kPCoreK, kPCoreK, 128),
-                    sw128_desc(va + 2 * n * kBlkChunk + k * 2048, kBlkChunk, 1024), kIdescPV,
-                    (k > 0 || !first) ? 1u : 0u);
+        pair_mma_ss(c.tmem + 256 * n, pd + k * (2 * kPCoreK >> 4), vd + (2 * n * kBlkChunk >> 4) + k * (2048 >> 4),
+                    kIdescPV, (k > 0 || !first) ? 1u : 0u);
     pair_commit(bar_addr(bars->v_empty[s]), kValueMask);
     if (last)
-      post_request(c, kReqFinal | static_cast<uint32_t>(r));  // the epilogues release the record
+      post_request(c, kReqFinal | r);  // the epilogues release the record
     else
       pair_commit(bar_addr(bars->p_empty[r]), kScoreMask);
   }
@@ -697,16 +698,14 @@ __device__ bool value_mma_segment(const Ctx& c, const Seg& g, uint32_t seg, uint
 }
 
 __device__ void value_mma(const Ctx& c) {
-  Walker w;
-  w.init(*c.p, c.engine);
-  Seg g;
-  uint32_t it = 0, seg = 0, ncorr = 0;
-  while (w.next(g)) {
-    int ok = 1;
-    if (c.lane == 0) ok = value_mma_segment(c, g, seg, it, ncorr) ? 1 : 0;
-    if (!__shfl_sync(0xffffffffu, ok, 0)) return;
-    ++seg;
+  if (elect_one()) {
+    Walker w;
+    w.init(*c.p, c.engine);
+    Seg g;
+    uint32_t it = 0, seg = 0, ncorr = 0;
+    while (w.next(g) && value_mma_segment(c, g, seg, it, ncorr)) ++seg;
   }
+  __syncwarp();
 }
 
 // Latent column of TMEM column c: every MMA's N = 256 columns are 128 of each

@@ -11,6 +11,17 @@
 namespace mla {
 namespace sm100 {
 
+// One thread of the warp (all lanes call it).  MMAs belong in a region chosen
+// by this election: the compiler then knows that one thread runs it and keeps
+// descriptors in uniform registers.  Measured with M = 256, N = 256: 128
+// cycles per MMA (the pipe's rate) against 186-237 in a region of `lane == 0`,
+// where the issue is the bound whatever N.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // One warp of each CTA of the pair calls these.
 __device__ __forceinline__ void pair_tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
