@@ -52,7 +52,7 @@ constexpr int kPassBlocks = 4;                // blocks per QK pass (N = 256)
 constexpr int kChunks = kRow / 64;            // 64-column chunks of a row
 constexpr int kKSlots = 5;                    // score: ring of [128 tokens x 64] chunks
 constexpr int kVSlots = 4;                    // value: ring of [64 tokens x 256] half blocks
-constexpr int kNP = 5;                        // P records in flight
+constexpr int kNP = 4;                        // P records in flight (5 measured the same, 3 are 15 % slower)
 
 constexpr uint32_t kQChunk = 128 * 128;       // [128 rows x 64] bf16
 constexpr uint32_t kBlkChunk = 64 * 128;      // [64 tokens x 64] bf16
@@ -104,8 +104,11 @@ __host__ __device__ constexpr uint32_t q_off(int ch) { return kQOff + ch * kQChu
 __host__ __device__ constexpr uint32_t k_slot_off(int s) { return kQOff + kChunks * kQChunk + s * kKSlot; }
 __host__ __device__ constexpr uint32_t v_slot_off(int s) { return 1024 + s * kVSlot; }
 __host__ __device__ constexpr uint32_t rec_off(int r) { return 1024 + kVSlots * kVSlot + r * kRecBytes; }
+// value: every epilogue warp's staging of 32 rows x 64 bytes of output
+constexpr uint32_t kStageBytes = 32 * 64;
+__host__ __device__ constexpr uint32_t stage_off(int w) { return rec_off(kNP) + w * kStageBytes; }
 constexpr uint32_t kScoreSmem = k_slot_off(kKSlots);
-constexpr uint32_t kValueSmem = rec_off(kNP);
+constexpr uint32_t kValueSmem = stage_off(8);
 // the dynamic shared memory of a kernel without static shared memory starts
 // at a multiple of 1024 here; the kernel checks it
 constexpr uint32_t kSmemBytes = kScoreSmem > kValueSmem ? kScoreSmem : kValueSmem;
@@ -125,7 +128,21 @@ struct Seg {
   int slot;        // partial slot, or -1 when the piece is the whole tile
 };
 
-// Tile holding concatenated block x: the last t with pre[t] <= x and a block.
+// The axis that is cut: every tile that reads the cache takes kTileUnits units
+// (what starting and finishing a tile costs next to a block) and one per block,
+// its blocks last.  Without that charge an engine that gets many short tiles
+// takes far longer than one with a single long tile.
+constexpr int kTileUnits = 8;
+// An engine gets at least this many units: fewer engines than that leave the
+// merge less to read than they save.
+constexpr int kMinUnits = 16;
+
+__device__ __forceinline__ int engines_of(const ChunkParams& p, long long total) {
+  const long long most = (total + kMinUnits - 1) / kMinUnits;
+  return most < p.P ? static_cast<int>(most) : p.P;
+}
+
+// Tile holding unit x: the last t with pre[t] <= x that has units.
 __device__ __forceinline__ int tile_of(const long long* pre, int nt, long long x) {
   int lo = 0, hi = nt;  // pre[lo] <= x < pre[hi]
   while (hi - lo > 1) {
@@ -135,12 +152,16 @@ __device__ __forceinline__ int tile_of(const long long* pre, int nt, long long x
   return lo;
 }
 
+// Inlined, as are the roles: state passed by reference to a real call would
+// live in local memory, whose cache next to 227 KB of shared memory holds a
+// fraction of the threads' frames (measured: an L2 round trip per access, 6.5
+// us instead of 4.9 us for a tile's output).
 struct Walker {
   const ChunkParams* p;
   long long s, e;
   int t, nt, engine, count;
 
-  __device__ __noinline__ void init(const ChunkParams& pp, int engine_) {
+  __device__ __forceinline__ void init(const ChunkParams& pp, int engine_) {
     p = &pp;
     engine = engine_;
     nt = *pp.n_tiles;
@@ -148,23 +169,20 @@ struct Walker {
     t = nt;
     s = e = 0;
     const long long total = pp.pre[nt];
-    const int P = total < pp.P ? static_cast<int>(total) : pp.P;
+    const int P = engines_of(pp, total);
     if (engine >= P) return;
     s = range_start(engine, total, P);
     e = range_start(engine + 1, total, P);
     t = tile_of(pp.pre, nt, s);
   }
 
-  __device__ __noinline__ bool next(Seg& g) {
-    while (t < nt) {
-      const long long a = p->pre[t], z = p->pre[t + 1];
-      if (a >= e) return false;
-      if (z == a || z <= s) {  // no cached token, or before the range
-        ++t;
-        continue;
-      }
+  __device__ __forceinline__ bool next(Seg& g) {
+    for (; t < nt; ++t) {
+      const long long a = p->pre[t] + kTileUnits, z = p->pre[t + 1];
       const int4 info = p->tiles[t];
+      if (a - kTileUnits >= e) return false;
       const long long lo = s > a ? s : a, hi = e < z ? e : z;
+      if (lo >= hi) continue;  // no cached token, or none of its blocks in the range
       g.row0 = info.x;
       g.rows = info.y;
       g.b = info.z;
@@ -195,13 +213,14 @@ __device__ __forceinline__ uint32_t bar_addr(const uint64_t& b) { return smem_u3
 struct BlockCursor {
   const int32_t* row;
   int nblk, base, cached;
-  __device__ void reset(const ChunkParams& p, const Seg& g) {
+  // Fetches the segment's first ids at once, ahead of their use.
+  __device__ __forceinline__ void reset(const ChunkParams& p, const Seg& g, int lane) {
     row = p.block_table + size_t(g.b) * p.max_blocks;
     nblk = nblocks_of(g.len);
-    base = -64;
-    cached = -1;
+    base = g.blk_lo;
+    cached = (base + lane < nblk) ? row[base + lane] : -1;
   }
-  __device__ int id(int j, int lane) {
+  __device__ __forceinline__ int id(int j, int lane) {
     if (j < base || j >= base + 32) {
       base = j;
       cached = (j + lane < nblk) ? row[j + lane] : -1;
@@ -227,7 +246,7 @@ __device__ __forceinline__ int blocks_per_cta(int nb) { return nb > 2 ? 2 : 1; }
 
 // ------------------------------------------------------------------ score pair
 
-__device__ void score_tma_k(const Ctx& c, const CUtensorMap* kmap) {
+__device__ __forceinline__ void score_tma_k(const Ctx& c, const CUtensorMap* kmap) {
   const ChunkParams& p = *c.p;
   Walker w;
   w.init(p, c.engine);
@@ -236,9 +255,19 @@ __device__ void score_tma_k(const Ctx& c, const CUtensorMap* kmap) {
   uint32_t fit = 0;
   const uint32_t full0 = map_to_rank(bar_addr(c.bars->k_full[0]), 0);
   if (c.lane == 0) prefetch_tmap(kmap);
-  while (w.next(g)) {
-    cur.reset(p, g);
+  bool more = w.next(g);
+  if (more) cur.reset(p, g, c.lane);
+  while (more) {
+    Seg gn = g;
+    BlockCursor cn = cur;
     for (int j = g.blk_lo; j < g.blk_hi; j += kPassBlocks) {
+      if (j == g.blk_lo + kPassBlocks || j + kPassBlocks >= g.blk_hi) {
+        // the next segment's records, while the ring is full
+        if (j == g.blk_lo + kPassBlocks || g.blk_hi - g.blk_lo <= kPassBlocks) {
+          more = w.next(gn);
+          if (more) cn.reset(p, gn, c.lane);
+        }
+      }
       const int nb = min(kPassBlocks, g.blk_hi - j);
       const int per = blocks_per_cta(nb);
       int blk[2] = {0, 0};
@@ -271,10 +300,12 @@ __device__ void score_tma_k(const Ctx& c, const CUtensorMap* kmap) {
         __syncwarp();
       }
     }
+    g = gn;
+    cur = cn;
   }
 }
 
-__device__ void score_tma_q(const Ctx& c, const CUtensorMap* qmap) {
+__device__ __forceinline__ void score_tma_q(const Ctx& c, const CUtensorMap* qmap) {
   const ChunkParams& p = *c.p;
   Walker w;
   w.init(p, c.engine);
@@ -300,7 +331,7 @@ __device__ void score_tma_q(const Ctx& c, const CUtensorMap* qmap) {
 // The elected thread of rank 0.  The barrier of the next chunk is probed
 // before the current chunk's MMAs are issued: a probe behind them would wait
 // for their issue and leave the pipe idle meanwhile.
-__device__ bool score_mma_segment(const Ctx& c, const Seg& g, uint32_t seg, uint32_t& slot, uint32_t& phase,
+__device__ __forceinline__ bool score_mma_segment(const Ctx& c, const Seg& g, uint32_t seg, uint32_t& slot, uint32_t& phase,
                                   uint32_t& pit) {
   Barriers* bars = c.bars;
   const uint32_t k_full0 = bar_addr(bars->k_full[0]), k_empty0 = bar_addr(bars->k_empty[0]);
@@ -334,7 +365,7 @@ __device__ bool score_mma_segment(const Ctx& c, const Seg& g, uint32_t seg, uint
   return true;
 }
 
-__device__ void score_mma(const Ctx& c) {
+__device__ __forceinline__ void score_mma(const Ctx& c) {
   if (elect_one()) {
     Walker w;
     w.init(*c.p, c.engine);
@@ -356,7 +387,7 @@ __device__ __forceinline__ bool xchg(const Ctx& c, int q4, int half, int h, uint
   return true;
 }
 
-__device__ void score_softmax(const Ctx& c) {
+__device__ __forceinline__ void score_softmax(const Ctx& c) {
   const ChunkParams& p = *c.p;
   const int q4 = c.warp & 3;           // TMEM lane quadrant
   const int half = (c.warp - 4) >> 2;  // blocks half, half + 2 of each pass
@@ -378,7 +409,7 @@ __device__ void score_softmax(const Ctx& c) {
   uint32_t it = 0, pit = 0, xit = 0;
   bool alive = true;
   while (alive && w.next(g)) {
-    cur.reset(p, g);
+    cur.reset(p, g, c.lane);
     // this row's query token sees the tile's length without its last
     // tokens' rows; padding rows see nothing
     const int row = 128 * c.rank + h;
@@ -528,7 +559,7 @@ __device__ void score_softmax(const Ctx& c) {
 
 // ------------------------------------------------------------------ value pair
 
-__device__ void value_tma(const Ctx& c, const CUtensorMap* kmap) {
+__device__ __forceinline__ void value_tma(const Ctx& c, const CUtensorMap* kmap) {
   const ChunkParams& p = *c.p;
   Walker w;
   w.init(p, c.engine);
@@ -537,9 +568,16 @@ __device__ void value_tma(const Ctx& c, const CUtensorMap* kmap) {
   uint32_t vit = 0;
   const int col0 = 256 * (c.rank - 2);  // this CTA's half of the latent
   if (c.lane == 0) prefetch_tmap(kmap);
-  while (w.next(g)) {
-    cur.reset(p, g);
+  bool more = w.next(g);
+  if (more) cur.reset(p, g, c.lane);
+  while (more) {
+    Seg gn = g;
+    BlockCursor cn = cur;
     for (int j = g.blk_lo; j < g.blk_hi; ++j, ++vit) {
+      if (j + 1 == g.blk_hi) {
+        more = w.next(gn);
+        if (more) cn.reset(p, gn, c.lane);
+      }
       int blk;
       block_rows(p, g, cur, j, c.lane, &blk);
       const int s = vit % kVSlots;
@@ -553,6 +591,8 @@ __device__ void value_tma(const Ctx& c, const CUtensorMap* kmap) {
       }
       __syncwarp();
     }
+    g = gn;
+    cur = cn;
   }
 }
 
@@ -568,7 +608,7 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t two) {
 // that sees such a row has NaN or infinite scores, hence NaN probabilities,
 // and gets its NaN from those, while one that does not see it (P = 0) must
 // not meet 0 * NaN.
-__device__ void value_fixup(const Ctx& c) {
+__device__ __forceinline__ void value_fixup(const Ctx& c) {
   const ChunkParams& p = *c.p;
   Walker w;
   w.init(p, c.engine);
@@ -577,7 +617,7 @@ __device__ void value_fixup(const Ctx& c) {
   uint32_t vit = 0;
   const uint32_t ready0 = map_to_rank(bar_addr(c.bars->v_ready[0]), 2);
   while (w.next(g)) {
-    cur.reset(p, g);
+    cur.reset(p, g, c.lane);
     const int all_see = g.len - (g.rows - 1) / p.H;  // tokens that every row of the tile sees
     for (int j = g.blk_lo; j < g.blk_hi; ++j, ++vit) {
       int blk;
@@ -616,7 +656,7 @@ __device__ void value_fixup(const Ctx& c) {
 // whether a row of it asks for a rescale.  P was written by asynchronous
 // stores of the score CTA: the proxy fence here makes it visible to the MMAs,
 // off the issuing thread's path.
-__device__ void value_relay(const Ctx& c) {
+__device__ __forceinline__ void value_relay(const Ctx& c) {
   Walker w;
   w.init(*c.p, c.engine);
   Seg g;
@@ -656,7 +696,7 @@ __device__ __forceinline__ void post_request(const Ctx& c, uint32_t req) {
 
 // The elected thread of rank 2; the next block's barriers are probed before
 // the current block's MMAs are issued.
-__device__ bool value_mma_segment(const Ctx& c, const Seg& g, uint32_t seg, uint32_t& it, uint32_t& ncorr) {
+__device__ __forceinline__ bool value_mma_segment(const Ctx& c, const Seg& g, uint32_t seg, uint32_t& it, uint32_t& ncorr) {
   Barriers* bars = c.bars;
   const uint64_t p0 = plain_desc(c.base + rec_off(0), kPCoreK, 128);
   const uint64_t v0 = sw128_desc(c.base + v_slot_off(0), kBlkChunk, 1024);
@@ -697,7 +737,7 @@ __device__ bool value_mma_segment(const Ctx& c, const Seg& g, uint32_t seg, uint
   return true;
 }
 
-__device__ void value_mma(const Ctx& c) {
+__device__ __forceinline__ void value_mma(const Ctx& c) {
   if (elect_one()) {
     Walker w;
     w.init(*c.p, c.engine);
@@ -712,8 +752,29 @@ __device__ void value_mma(const Ctx& c) {
 // CTA's half.
 __device__ __forceinline__ int latent_of(int c) { return 256 * ((c >> 7) & 1) + 128 * (c >> 8) + (c & 127); }
 
+// Writes 64 bytes of each of the warp's 32 rows (lane = row, v = its bytes):
+// turned around in shared memory, so that a store of the warp fills eight
+// 64-byte pieces instead of touching 32 rows (measured: the output of a tile
+// 7.2 us when every lane stores its own row).  16-byte units are swizzled
+// against bank conflicts.  dst(r) is row r's address, or null for a padding row.
+template <class Dst>
+__device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint4 (&v)[4], Dst dst) {
+  const int sw = (lane >> 1) & 3;
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ sw) << 4)) = v[q];
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2), q = lane & 3;
+    uint8_t* at = dst(r);
+    if (at != nullptr)
+      *reinterpret_cast<uint4*>(at + 16 * q) = *reinterpret_cast<const uint4*>(stage + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+  }
+}
+
 // Thread = (row, half of the TMEM columns).
-__device__ void value_epilogue(const Ctx& c) {
+__device__ __forceinline__ void value_epilogue(const Ctx& c) {
   const ChunkParams& p = *c.p;
   const int q4 = c.warp & 3;
   const int half = (c.warp - 4) >> 2;
@@ -721,6 +782,9 @@ __device__ void value_epilogue(const Ctx& c) {
   const int row = 128 * (c.rank - 2) + h;
   const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
   const uint32_t ocol = 256 * half;
+  const uint32_t corr_done = map_to_rank(bar_addr(c.bars->corr_done), 2);
+  const uint32_t o_free = map_to_rank(bar_addr(c.bars->o_free), 2);
+  const uint32_t pempty0 = map_to_rank(bar_addr(c.bars->p_empty[0]), c.rank - 2);
   Walker w;
   w.init(p, c.engine);
   Seg g;
@@ -749,7 +813,7 @@ __device__ void value_epilogue(const Ctx& c) {
         }
         tc_fence_before();
         __syncwarp();
-        if (c.lane == 0) mbar_arrive_remote(bar_addr(c.bars->corr_done), 2);
+        if (c.lane == 0) mbar_arrive_cluster_relaxed(corr_done);
         continue;
       }
       const float m_fin = meta.y, l_fin = meta.z;
@@ -757,21 +821,23 @@ __device__ void value_epilogue(const Ctx& c) {
       if (c.lane == 0) mbar_arrive(bar_addr(c.bars->meta_done));
       if (c.warp == 4) {
         if (!warp_wait(bar_addr(c.bars->meta_done), nfinal & 1u, c.wc)) return;
-        if (c.lane == 0) mbar_arrive_remote(bar_addr(c.bars->p_empty[req & 0xffu]), c.rank - 2);
+        if (c.lane == 0) mbar_arrive_cluster_relaxed(pempty0 + 8 * (req & 0xffu));
       }
       ++nfinal;
       const bool live = row < g.rows;
       const float inv = l_fin > 0.f ? 1.f / l_fin : (l_fin == 0.f ? 0.f : l_fin);  // a NaN sum stays NaN
       const float lse = l_fin == 0.f ? -INFINITY : (m_fin + log2f(l_fin)) * 0.6931471805599453f;
-#pragma unroll 1
-      for (int ch = 0; ch < 8; ++ch) {
-        uint32_t v[32];
-        tmem_ld32(c.tmem + lane_off + ocol + 32 * ch, v);
-        tmem_ld_wait();
-        if (!live) continue;
-        const int col = latent_of(ocol + 32 * ch);
-        if (g.slot < 0) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + (size_t(g.row0) + row) * kDc + col);
+      uint8_t* stage = c.gbase + stage_off(c.warp - 4);
+      const int row0 = 128 * (c.rank - 2) + q4 * 32;  // the warp's first row
+      if (g.slot < 0) {
+        // all of the row's half as bf16 in registers, so that the next tile's
+        // MMAs may start on O before the rows are stored
+        uint4 o[8][4];
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {
+          uint32_t v[32];
+          tmem_ld32(c.tmem + lane_off + ocol + 32 * ch, v);
+          tmem_ld_wait();
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t w4[4];
@@ -781,19 +847,46 @@ __device__ void value_epilogue(const Ctx& c) {
                                                         __uint_as_float(v[8 * q + 2 * e + 1]) * inv);
               w4[e] = *reinterpret_cast<uint32_t*>(&b2);
             }
-            dst[q] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+            o[ch][q] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
           }
-        } else {
-          float4* dst = reinterpret_cast<float4*>(p.o_part + (size_t(g.slot) * kTileRows + row) * kDc + col);
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            dst[q] = make_float4(__uint_as_float(v[4 * q]) * inv, __uint_as_float(v[4 * q + 1]) * inv,
-                                 __uint_as_float(v[4 * q + 2]) * inv, __uint_as_float(v[4 * q + 3]) * inv);
         }
+        tc_fence_before();
+        __syncwarp();
+        if (c.lane == 0) mbar_arrive_cluster_relaxed(o_free);
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {
+          const int col = latent_of(ocol + 32 * ch);
+          store_rows(stage, c.lane, o[ch], [&](int r) -> uint8_t* {
+            if (row0 + r >= g.rows) return nullptr;
+            return reinterpret_cast<uint8_t*>(p.out + (size_t(g.row0) + row0 + r) * kDc + col);
+          });
+        }
+      } else {
+#pragma unroll 1
+        for (int ch = 0; ch < 8; ++ch) {
+          uint32_t v[32];
+          tmem_ld32(c.tmem + lane_off + ocol + 32 * ch, v);
+          tmem_ld_wait();
+          const int col = latent_of(ocol + 32 * ch);
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            uint4 o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int e = 16 * part + 4 * q;
+              o[q] = make_uint4(__float_as_uint(__uint_as_float(v[e]) * inv), __float_as_uint(__uint_as_float(v[e + 1]) * inv),
+                                __float_as_uint(__uint_as_float(v[e + 2]) * inv), __float_as_uint(__uint_as_float(v[e + 3]) * inv));
+            }
+            store_rows(stage, c.lane, o, [&](int r) -> uint8_t* {
+              if (row0 + r >= g.rows) return nullptr;
+              return reinterpret_cast<uint8_t*>(p.o_part + (size_t(g.slot) * kTileRows + row0 + r) * kDc + col + 16 * part);
+            });
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (c.lane == 0) mbar_arrive_cluster_relaxed(o_free);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (c.lane == 0) mbar_arrive_remote(bar_addr(c.bars->o_free), 2);
       if (live && half == 0) {
         if (g.slot < 0)
           p.lse[size_t(g.row0) + row] = lse;
@@ -982,7 +1075,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
       // the tile's last token sees the sequence without the n - j - tok tokens behind it
       const int len = max(0, checked_len(p.seq_lens, lo, p.max_blocks, nullptr) - (n - j - tok));
       p.tiles[t] = make_int4((a + j) * p.H, tok * p.H, lo, len);
-      mine = nblocks_of(len);
+      mine = len > 0 ? nblocks_of(len) + kTileUnits : 0;
     }
     long long total;
     const long long incl = block_scan(mine, sums, &total);
@@ -1024,7 +1117,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkP
       fill_row(p, size_t(a) * p.H + r, -INFINITY, lane);
   }
   const long long total = p.pre[nt];
-  const int P = total < p.P ? static_cast<int>(total) : p.P;
+  const int P = engines_of(p, total);
   const int e1 = blockIdx.x + 1;  // the boundary between engines e1 - 1 and e1
   if (e1 >= P) return;
   const long long x = range_start(e1, total, P);
@@ -1032,45 +1125,59 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkP
   const long long a = p.pre[t], z = p.pre[t + 1];
   const long long s0 = range_start(e1 - 1, total, P);
   // merged at the boundary whose left engine holds the tile's first block
-  if (x == a || s0 > a) return;
+  if (x <= a + kTileUnits || s0 > a + kTileUnits) return;
   const int4 info = p.tiles[t];
   if (wrow >= info.y) return;
   const int last = engine_of(z - 1, total, P);
   const int n = last - (e1 - 1) + 1;
-  auto slot_of = [&](int i) { return 2 * (e1 - 1 + i) + (i == 0 && s0 != a ? 1 : 0); };
-  float M = -INFINITY;
-  for (int i = 0; i < n; ++i) {
-    const float v = p.lse_part[size_t(slot_of(i)) * kTileRows + wrow];
-    M = v != v ? v : fmaxf(M, v);
-    if (v != v) break;
+  // the first piece is its engine's second segment if the engine's range starts in an earlier tile
+  auto slot_of = [&](int i) { return 2 * (e1 - 1 + i) + (i == 0 && s0 < a ? 1 : 0); };
+  // 32 pieces at a time, one per lane
+  float M = -INFINITY, sum = 0.f;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    float v = -INFINITY;
+    if (i0 + lane < n) v = p.lse_part[size_t(slot_of(i0 + lane)) * kTileRows + wrow];
+    float m = v;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float Mn = fmaxf(M, m);
+    float e = Mn == -INFINITY ? 0.f : expf(v - Mn);  // NaN pieces make the sum NaN
+    if (v != v) e = v;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
+    sum = (M == -INFINITY ? 0.f : sum * expf(M - Mn)) + e;
+    M = Mn;
   }
   const size_t row = size_t(info.x) + wrow;
-  if (M == -INFINITY) {
+  if (M == -INFINITY && sum == 0.f) {
     fill_row(p, row, -INFINITY, lane);
     return;
   }
-  float sum = 0.f;
-  for (int i = 0; i < n; ++i) sum += expf(p.lse_part[size_t(slot_of(i)) * kTileRows + wrow] - M);
   const float L = M + logf(sum);
   float acc[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) acc[k] = 0.f;
-  for (int i = 0; i < n; ++i) {
-    const size_t r = size_t(slot_of(i)) * kTileRows + wrow;
-    const float li = p.lse_part[r];
-    if (li == -INFINITY) continue;
-    const float wgt = expf(li - L);
-    const float4* src = reinterpret_cast<const float4*>(p.o_part + r * kDc + lane * 16);
-    float4 v[4];
+  // two pieces in flight; an empty piece holds zeros and weighs exp(-inf) = 0
+  for (int i = 0; i < n; i += 2) {
+    float wgt[2];
+    float4 v[2][4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = src[q];
+    for (int u = 0; u < 2; ++u) {
+      const size_t r = size_t(slot_of(min(i + u, n - 1))) * kTileRows + wrow;
+      wgt[u] = i + u < n ? expf(p.lse_part[r] - L) : 0.f;
+      const float4* src = reinterpret_cast<const float4*>(p.o_part + r * kDc + lane * 16);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      acc[4 * q] += wgt * v[q].x;
-      acc[4 * q + 1] += wgt * v[q].y;
-      acc[4 * q + 2] += wgt * v[q].z;
-      acc[4 * q + 3] += wgt * v[q].w;
+      for (int q = 0; q < 4; ++q) v[u][q] = src[q];
     }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        acc[4 * q] += wgt[u] * v[u][q].x;
+        acc[4 * q + 1] += wgt[u] * v[u][q].y;
+        acc[4 * q + 2] += wgt[u] * v[u][q].z;
+        acc[4 * q + 3] += wgt[u] * v[u][q].w;
+      }
   }
   uint32_t pk[8];
 #pragma unroll

@@ -11,7 +11,7 @@ import pytest
 
 from tests.test_pipeline_protocol import Bar, _passes, _patterns
 
-K_SLOTS, V_SLOTS, N_REC, CHUNKS = 5, 4, 5, 9
+K_SLOTS, V_SLOTS, N_REC, CHUNKS = 5, 4, 4, 9
 
 
 def roles(segs, flags, counts):
