@@ -734,6 +734,7 @@ mla_status_t mla_cache_evict(const float* weight, const int32_t* slot_pos, const
   p.new_pos = new_pos;
   p.new_lens = new_lens;
   p.err = reinterpret_cast<uint32_t*>(wsb);
+  p.spin_limit = g_decode_wait_limit.load();
   p.n_moves = reinterpret_cast<int32_t*>(wsb + lay.n_moves);
   p.moves = reinterpret_cast<int2*>(wsb + lay.moves);
   return status_of(launch_evict(p, device_sms(), static_cast<cudaStream_t>(stream)));

@@ -167,6 +167,7 @@ struct EvictParams {
   int32_t* new_pos;
   int32_t* new_lens;
   uint32_t* err;
+  long long spin_limit;
   int32_t* n_moves;  // [B]
   int2* moves;       // [B, 32*max_blocks] (source slot, destination slot)
 };

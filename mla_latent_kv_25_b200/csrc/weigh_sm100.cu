@@ -24,6 +24,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "pair.cuh"
 #include "schedule.cuh"
 #include "sm100.cuh"
 
@@ -104,7 +105,7 @@ __device__ __forceinline__ void load_k_chunk(const CUtensorMap* kmap, uint32_t d
 }
 
 // The producer's loop over one segment (one thread).
-__device__ bool produce(const Ctx& c, const CUtensorMap* qmap, const CUtensorMap* kmap, const Segment& g,
+__device__ __forceinline__ bool produce(const Ctx& c, const CUtensorMap* qmap, const CUtensorMap* kmap, const Segment& g,
                         const Queries& q, uint32_t& rit, uint32_t& fit) {
   const WeighParams& p = *c.p;
   Bars* bars = c.bars;
@@ -143,35 +144,45 @@ __device__ bool produce(const Ctx& c, const CUtensorMap* qmap, const CUtensorMap
   return true;
 }
 
-__device__ bool multiply(const Ctx& c, const Segment& g, const Queries& q, uint32_t& rit, uint32_t& fit,
-                         uint32_t& ait) {
+// The MMA warp's loop over one segment (its elected thread); the next chunk's
+// barrier is probed before the current chunk's MMAs are issued.
+__device__ __forceinline__ bool multiply(const Ctx& c, int tiles, const Queries& q, uint32_t& rit, uint32_t& slot,
+                                         uint32_t& phase, uint32_t& ait) {
   Bars* bars = c.bars;
   const bool queries_stay = q.tiles == 1;
+  const uint32_t full0 = bar_addr(bars->ring_full[0]), empty0 = bar_addr(bars->ring_empty[0]);
+  const uint64_t res0 = sw128_desc(c.base + kResOff, 16, 1024), ring0 = sw128_desc(c.base + kRingOff, 16, 1024);
   auto wait_resident = [&]() {
     const bool ok = wait_phase(bar_addr(bars->res_full), rit & 1u, c.wc);
     ++rit;
     return ok;
   };
+  bool ready = false;
   if (queries_stay && !wait_resident()) return false;
-  for (int j = g.blk_lo; j < g.blk_hi; j += 2) {
+  for (int j = 0; j < tiles; ++j) {
     if (!queries_stay && !wait_resident()) return false;
     const int streams = queries_stay ? 1 : q.tiles;
     for (int i = 0; i < streams; ++i, ++ait) {
       const int buf = ait % kAcc;
       // the last tile of a sequence may have fewer rows (a multiple of 16)
       const uint32_t idesc = idesc_bf16(128, min(128, q.rows - 128 * i), false, false);
+      const uint32_t d = c.tmem + 128 * buf;
       if (!wait_phase(bar_addr(bars->acc_empty[buf]), ((ait / kAcc) & 1u) ^ 1u, c.wc)) return false;
       tc_fence_after();
-      for (int ch = 0; ch < kChunks; ++ch, ++fit) {
-        const int s = fit % kRing;
-        if (!wait_phase(bar_addr(bars->ring_full[s]), (fit / kRing) & 1u, c.wc)) return false;
-        const uint32_t res = c.base + kResOff + ch * kChunk, str = c.base + kRingOff + s * kChunk;
-        const uint32_t a = queries_stay ? str : res, bq = queries_stay ? res : str;
+#pragma unroll 1
+      for (int ch = 0; ch < kChunks; ++ch) {
+        if (!ready && !wait_phase(full0 + 8 * slot, phase, c.wc)) return false;
+        const uint32_t s = slot;
+        if (++slot == kRing) {
+          slot = 0;
+          phase ^= 1u;
+        }
+        ready = mbar_test_wait(full0 + 8 * slot, phase);
+        const uint64_t res = res0 + static_cast<uint32_t>(ch) * (kChunk >> 4), str = ring0 + s * (kChunk >> 4);
+        const uint64_t a = queries_stay ? str : res, bq = queries_stay ? res : str;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ss(c.tmem + 128 * buf, sw128_desc(a + kk * 32, 16, 1024), sw128_desc(bq + kk * 32, 16, 1024), idesc,
-                 (ch | kk) ? 1u : 0u);
-        mma_commit(bar_addr(bars->ring_empty[s]));
+        for (int kk = 0; kk < 4; ++kk) mma_ss(d, a + 2 * kk, bq + 2 * kk, idesc, (ch | kk) ? 1u : 0u);
+        mma_commit(empty0 + 8 * s);
       }
       mma_commit(bar_addr(bars->acc_full[buf]));
     }
@@ -190,7 +201,7 @@ __device__ __forceinline__ void load_lse(const WeighParams& p, const Queries& q,
   }
 }
 
-__device__ bool accumulate(const Ctx& c, const Segment& g, const Queries& q, uint32_t& ait) {
+__device__ __forceinline__ bool accumulate(const Ctx& c, const Segment& g, const Queries& q, uint32_t& ait) {
   const WeighParams& p = *c.p;
   Bars* bars = c.bars;
   const int quad = c.warp & 3;
@@ -303,17 +314,21 @@ weigh_sm100_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
 
   SegWalker w;
   w.init(p.seq_lens, p.B, p.max_blocks, gridDim.x, blockIdx.x);
-  Segment g;
-  uint32_t rit = 0, fit = 0, ait = 0;
-  while (w.next(g)) {
+  Segment gs;
+  uint32_t rit = 0, fit = 0, ait = 0, slot = 0, phase = 0;
+  while (w.next(gs)) {
+    const Segment g = gs;  // in registers, not behind the walker's reference
     const Queries q = queries_of(p, g.b);
     int ok = 1;
     if (warp == 0) {
       if (q.tiles > 0 && lane == 0) ok = produce(c, &qmap, &kmap, g, q, rit, fit) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
     } else if (warp == 1) {
-      if (q.tiles > 0 && lane == 0) ok = multiply(c, g, q, rit, fit, ait) ? 1 : 0;
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      // counters live in the elected thread, the same one every time
+      if (q.tiles > 0 && elect_one()) {
+        if (!multiply(c, (g.blk_hi - g.blk_lo + 1) / 2, q, rit, slot, phase, ait)) ok = 0;
+      }
+      ok = __all_sync(0xffffffffu, ok);
     } else {
       ok = accumulate(c, g, q, ait) ? 1 : 0;
     }
