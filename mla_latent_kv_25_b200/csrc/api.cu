@@ -685,14 +685,12 @@ mla_status_t mla_cache_weigh(const void* q, const int32_t* q_offsets, int T, con
   p.weight_in = weight_in;
   p.weight_out = weight_out;
   p.spin_limit = g_decode_wait_limit.load();
-  const int sms = device_sms();
-  if (sms < 1) return fail_with("no streaming multiprocessor count for the current device");
   CUtensorMap qmap, kmap;
   // without queries the map is never read through: any valid base does
-  if (!encode_rows_map(&qmap, T > 0 ? q : cache, T > 0 ? uint64_t(T) * H : 128) ||
+  if (!encode_bf16_map(&qmap, T > 0 ? q : cache, T > 0 ? uint64_t(T) * H : kBlock, kRow, kRow * 2) ||
       !encode_bf16_map(&kmap, cache, uint64_t(num_blocks) * kBlock, kRow, kRow * 2))
     return fail_with("tensor map encoding failed");
-  return status_of(launch_weigh(p, qmap, kmap, sms, static_cast<cudaStream_t>(stream)));
+  return status_of(launch_weigh(p, qmap, kmap, static_cast<cudaStream_t>(stream)));
 }
 
 size_t mla_evict_workspace_bytes(int B, int max_blocks_per_seq) {

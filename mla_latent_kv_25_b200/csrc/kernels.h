@@ -129,7 +129,8 @@ struct ChunkParams {
   float* lse_part;     // [2P][256]
   float* o_part;       // [2P][256][512]
 };
-// Plan, attention and merge kernels.  kmap, qmap: as for launch_weigh.
+// Plan, attention and merge kernels.  kmap as for launch_weigh; qmap: q as
+// [T*H, 576] with 64 x 128 boxes.
 cudaError_t launch_chunk_sm100(const ChunkParams& p, const CUtensorMap& kmap, const CUtensorMap& qmap,
                                cudaStream_t stream);
 int chunk_sm100_max_clusters();
@@ -147,9 +148,9 @@ struct WeighParams {
   float* weight_out;
   long long spin_limit;
 };
-// qmap: q as [max(T, 1)*H, 576] with 64 x 128 boxes; kmap: the cache as
-// [num_blocks*64, 576] with 64 x 64 boxes; both 128-byte swizzled.
-cudaError_t launch_weigh(const WeighParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap, int num_sms,
+// qmap: q as [T*H, 576]; kmap: the cache as [num_blocks*64, 576]; both with
+// 64 x 64 boxes, 128-byte swizzled.
+cudaError_t launch_weigh(const WeighParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
                          cudaStream_t stream);
 // Copies mla_cache_weigh's error word to *bits and clears it (synchronises `stream`).
 cudaError_t weigh_take_error(uint32_t* bits, cudaStream_t stream);

@@ -1,22 +1,25 @@
 // Attention weight per cached token on tcgen05 tensor cores:
 //   weight_out[b,t] = weight_in[b,t] + sum_{j,h} exp(scale q[j,h] . row_t - lse[j,h])
 //
-// Cached tokens are the M = 128 dimension (two 64-token blocks), query rows
-// (token j, head h) the N dimension, so a TMEM lane holds one token's scores
-// and the sum over heads and queries is a sum along the lane: no shuffles, no
-// atomics, one fixed order.
+// Cached tokens are the M dimension, query rows (token j, head h) the N
+// dimension, so a TMEM lane holds one token's scores and the sum over heads
+// and queries is a sum along the lane: no shuffles, no atomics, one fixed
+// order.  A pair of CTAs (cta_group::2) takes M = 256 tokens, 128 each; the
+// query rows are split over the two CTAs' shared memory, so every row is
+// fetched once per 256 tokens.
 //
 // Bound: with one query token per sequence the cache is read once and the
 // kernel is bound by HBM (1152 bytes per token); with many query tokens by
-// the tensor pipe.  A persistent CTA per SM takes a contiguous range of the
-// concatenated block list (SegWalker).  Both operands of a tile are 128 rows
-// of 576 bf16 in nine 128-byte-swizzled chunks, so one may stay in shared
-// memory while the other streams through a ring of 16 KB chunks:
-//   a sequence with one query tile (<= 128 rows): the queries stay, the cache
-//     streams past them (every cached row is fetched once);
-//   more query tiles: a tile of 128 tokens stays, the queries stream (from L2).
+// the tensor pipe (and L2, which has to deliver 32 bytes per clock and SM).
+// Each pair takes a contiguous range of the concatenated block list
+// (SegWalker).  One operand of a tile stays in shared memory while the other
+// streams through a ring of 16 KB chunks [128 rows x 64 columns]:
+//   a sequence with at most 128 query rows: the queries stay (64 rows per
+//     CTA), the cache streams past them through nine slots;
+//   more query rows: 128 tokens per CTA stay, the queries stream 256 rows at
+//     a time through five slots.
 //
-// w0: TMA; w1: MMA (one thread), TMEM; w2-5: epilogue, thread = token.
+// w0: TMA; w1: MMA (one thread of rank 0), TMEM; w2-5: epilogue, thread = token.
 #include <cuda.h>
 #include <math.h>
 
@@ -39,33 +42,51 @@ namespace {
 using namespace sm100;
 
 constexpr int kThreads = 192;
-constexpr int kTileTok = 128;                 // tokens per tile (two blocks)
+constexpr int kTileBlocks = 4;                // blocks of a tile, two per CTA
+constexpr int kStayRows = 128;                // queries stay up to this many rows
+constexpr int kStreamRows = 256;              // else they stream in tiles of this many
 constexpr int kChunks = kRow / 64;            // 64-column chunks of a row
 constexpr uint32_t kChunk = 128 * 128;        // [128 rows x 64] bf16
-constexpr int kRing = 5;
-constexpr int kAcc = 2;                       // accumulators [128 x 128] fp32 in TMEM
-constexpr uint32_t kTmemCols = 256;
+constexpr uint32_t kHalf = kChunk / 2;        // [64 rows x 64]
+constexpr int kRingMax = 9;                   // slots while the queries stay
+constexpr int kRingMin = 5;                   // slots while the tokens stay
+constexpr int kAcc = 2;                       // accumulators [128 x 256] fp32 in TMEM
+constexpr uint32_t kTmemCols = 512;
+constexpr uint16_t kBoth = 0x3;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Barriers live at the same offsets in both CTAs; "leader" ones are used in
+// rank 0 only and count both CTAs' bytes or arrivals.
 struct Bars {
-  uint64_t ring_full[kRing], ring_empty[kRing];
-  uint64_t res_full, res_empty;
-  uint64_t acc_full[kAcc], acc_empty[kAcc];
+  uint64_t ring_full[kRingMax];   // leader
+  uint64_t ring_empty[kRingMax];  // commit to both
+  uint64_t res_full;              // leader
+  uint64_t res_empty;             // commit to both
+  uint64_t acc_full[kAcc];        // commit to both
+  uint64_t acc_empty[kAcc];       // leader
+  uint64_t lse_full[2];           // this CTA's epilogue warps wrote their shares
   uint32_t tmem_base;
   int abort;
 };
 static_assert(sizeof(Bars) <= 1024, "barrier block too large");
 
-constexpr uint32_t kResOff = 1024;
-constexpr uint32_t kRingOff = kResOff + kChunks * kChunk;
-constexpr uint32_t kSmem = kRingOff + kRing * kChunk + 1024;
-static_assert(kSmem <= 232448, "shared memory budget");
+constexpr uint32_t kLseOff = 1024;              // float [2][kStreamRows]: a query tile's lse, base 2
+constexpr uint32_t kResOff = kLseOff + 2 * kStreamRows * 4;
+// the resident operand: 64 query rows or 128 tokens; the ring behind it
+__host__ __device__ constexpr uint32_t ring_off(bool queries_stay) {
+  return kResOff + kChunks * (queries_stay ? kHalf : kChunk);
+}
+// the dynamic shared memory of a kernel without static shared memory starts
+// at a multiple of 1024 here; the kernel checks it
+constexpr uint32_t kSmem = ring_off(false) + kRingMin * kChunk;
+static_assert(ring_off(true) + kRingMax * kChunk <= kSmem && kSmem <= 232448, "shared memory budget");
 
 struct Queries {
   int n;        // query tokens of the sequence
   int row0;     // first row of q
   int rows;     // n * H
-  int tiles;    // of 128 rows
+  bool stay;    // one tile of at most kStayRows rows, held in shared memory
+  int tiles;
 };
 
 __device__ __forceinline__ Queries queries_of(const WeighParams& p, int b) {
@@ -74,8 +95,14 @@ __device__ __forceinline__ Queries queries_of(const WeighParams& p, int b) {
   q.n = a >= 0 && e >= a && e <= p.T ? e - a : 0;
   q.row0 = a * p.H;
   q.rows = q.n * p.H;
-  q.tiles = (q.rows + 127) / 128;
+  q.stay = q.rows <= kStayRows;
+  q.tiles = q.stay ? (q.rows > 0 ? 1 : 0) : (q.rows + kStreamRows - 1) / kStreamRows;
   return q;
+}
+
+// Rows of query tile i: a multiple of 16, half of them from each CTA.
+__device__ __forceinline__ int tile_rows(const Queries& q, int i) {
+  return q.stay ? q.rows : min(kStreamRows, q.rows - kStreamRows * i);
 }
 
 struct Ctx {
@@ -84,166 +111,218 @@ struct Ctx {
   Bars* bars;
   uint32_t tmem;
   WaitCtx wc;
-  int warp, lane;
+  int rank, warp, lane;
 };
 
 __device__ __forceinline__ uint32_t bar_addr(const uint64_t& b) { return smem_u32(&b); }
 
+// Position in the ring.  The slot count depends on the operand that stays, so
+// every slot has a phase of its own; a segment with the other operand starts
+// at slot 0 again (its first resident load waits for all earlier MMAs, so
+// every slot is free then).
+struct Ring {
+  int slot = 0;
+  uint32_t phases = 0;  // bit s: parity of slot s's next fill
+  bool stay = false;
+  __device__ __forceinline__ bool mode(bool queries_stay) {
+    const bool switched = stay != queries_stay;
+    if (switched) slot = 0;
+    stay = queries_stay;
+    return switched;
+  }
+  __device__ __forceinline__ uint32_t phase() const { return (phases >> slot) & 1u; }
+  __device__ __forceinline__ void next() {
+    phases ^= 1u << slot;
+    slot = slot + 1 == (stay ? kRingMax : kRingMin) ? 0 : slot + 1;
+  }
+};
+
+// A block of the tile that is safe to load; missing blocks load block 0 (both
+// CTAs always load, so that neither runs ahead of the other).
 __device__ __forceinline__ int safe_block(const WeighParams& p, const Segment& g, int j) {
   const int id = j < g.blk_hi ? p.block_table[size_t(g.b) * p.max_blocks + j] : 0;
   return id >= 0 && id < p.num_blocks ? id : 0;
 }
 
-// One 128-row operand chunk: query rows from `row`, or the two blocks of a tile.
-__device__ __forceinline__ void load_q_chunk(const CUtensorMap* qmap, uint32_t dst, int ch, int row, uint32_t bar) {
-  tma_load_2d(dst, qmap, 64 * ch, row, bar);
-}
-__device__ __forceinline__ void load_k_chunk(const CUtensorMap* kmap, uint32_t dst, int ch, int blk0, int blk1,
-                                             uint32_t bar) {
-  tma_load_2d(dst, kmap, 64 * ch, blk0 * kBlock, bar);
-  tma_load_2d(dst + kChunk / 2, kmap, 64 * ch, blk1 * kBlock, bar);
-}
-
-// The producer's loop over one segment (one thread).
-__device__ __forceinline__ bool produce(const Ctx& c, const CUtensorMap* qmap, const CUtensorMap* kmap, const Segment& g,
-                        const Queries& q, uint32_t& rit, uint32_t& fit) {
+// The producer's loop over one segment (one thread of each CTA); bytes are
+// counted on rank 0's barriers, announced there by rank 0 for both CTAs.
+__device__ __forceinline__ bool produce(const Ctx& c, const CUtensorMap* qmap, const CUtensorMap* kmap,
+                                        const Segment& g, const Queries& q, uint32_t& rit, Ring& ring) {
   const WeighParams& p = *c.p;
   Bars* bars = c.bars;
-  const bool queries_stay = q.tiles == 1;
-  auto resident = [&]() {
+  const uint32_t res_bar = map_to_rank(bar_addr(bars->res_full), 0);
+  const uint32_t full0 = map_to_rank(bar_addr(bars->ring_full[0]), 0);
+  const bool switched = ring.mode(q.stay);
+  const uint32_t ring0 = c.base + ring_off(q.stay);
+  auto resident = [&](uint32_t bytes) {
     const bool ok = wait_phase(bar_addr(bars->res_empty), (rit & 1u) ^ 1u, c.wc);
     ++rit;
-    if (ok) mbar_arrive_expect_tx(bar_addr(bars->res_full), kChunks * kChunk);
+    if (ok && c.rank == 0) mbar_arrive_expect_tx(bar_addr(bars->res_full), 2 * bytes);
     return ok;
   };
-  const uint32_t res_bar = bar_addr(bars->res_full);
-  if (queries_stay) {
-    if (!resident()) return false;
-    for (int ch = 0; ch < kChunks; ++ch) load_q_chunk(qmap, c.base + kResOff + ch * kChunk, ch, q.row0, res_bar);
+  auto load_queries = [&]() {
+    if (!resident(kChunks * kHalf)) return false;
+    for (int ch = 0; ch < kChunks; ++ch)
+      pair_tma_load_2d(c.base + kResOff + ch * kHalf, qmap, 64 * ch, q.row0 + c.rank * (q.rows / 2), res_bar);
+    return true;
+  };
+  // The next sequence's queries have to wait for all of the previous one's
+  // MMAs; its first tile (as many chunks as slots) need not, unless the ring
+  // is laid out anew.
+  bool queries_due = q.stay;
+  if (queries_due && switched) {
+    if (!load_queries()) return false;
+    queries_due = false;
   }
-  for (int j = g.blk_lo; j < g.blk_hi; j += 2) {
-    const int b0 = safe_block(p, g, j), b1 = safe_block(p, g, j + 1);
-    if (!queries_stay) {
-      if (!resident()) return false;
-      for (int ch = 0; ch < kChunks; ++ch) load_k_chunk(kmap, c.base + kResOff + ch * kChunk, ch, b0, b1, res_bar);
-    }
-    const int streams = queries_stay ? 1 : q.tiles;
-    for (int i = 0; i < streams; ++i)
-      for (int ch = 0; ch < kChunks; ++ch, ++fit) {
-        const int s = fit % kRing;
-        if (!wait_phase(bar_addr(bars->ring_empty[s]), ((fit / kRing) & 1u) ^ 1u, c.wc)) return false;
-        const uint32_t full = bar_addr(bars->ring_full[s]);
-        const uint32_t dst = c.base + kRingOff + s * kChunk;
-        mbar_arrive_expect_tx(full, kChunk);
-        if (queries_stay)
-          load_k_chunk(kmap, dst, ch, b0, b1, full);
-        else
-          load_q_chunk(qmap, dst, ch, q.row0 + 128 * i, full);
+  for (int j = g.blk_lo; j < g.blk_hi; j += kTileBlocks) {
+    const int y0 = safe_block(p, g, j + 2 * c.rank) * kBlock, y1 = safe_block(p, g, j + 2 * c.rank + 1) * kBlock;
+    if (!q.stay) {
+      if (!resident(kChunks * kChunk)) return false;
+      for (int ch = 0; ch < kChunks; ++ch) {
+        pair_tma_load_2d(c.base + kResOff + ch * kChunk, kmap, 64 * ch, y0, res_bar);
+        pair_tma_load_2d(c.base + kResOff + ch * kChunk + kHalf, kmap, 64 * ch, y1, res_bar);
       }
+    }
+    const int streams = q.stay ? 1 : q.tiles;
+    for (int i = 0; i < streams; ++i) {
+      const int row = q.row0 + kStreamRows * i + c.rank * (tile_rows(q, i) / 2);
+      for (int ch = 0; ch < kChunks; ++ch) {
+        if (!wait_phase(bar_addr(bars->ring_empty[ring.slot]), ring.phase() ^ 1u, c.wc)) return false;
+        const uint32_t full = full0 + 8 * ring.slot;
+        const uint32_t dst = ring0 + ring.slot * kChunk;
+        if (c.rank == 0) mbar_arrive_expect_tx(bar_addr(bars->ring_full[ring.slot]), 2 * kChunk);
+        pair_tma_load_2d(dst, q.stay ? kmap : qmap, 64 * ch, q.stay ? y0 : row, full);
+        pair_tma_load_2d(dst + kHalf, q.stay ? kmap : qmap, 64 * ch, q.stay ? y1 : row + 64, full);
+        ring.next();
+      }
+      if (queries_due) {
+        if (!load_queries()) return false;
+        queries_due = false;
+      }
+    }
   }
   return true;
 }
 
-// The MMA warp's loop over one segment (its elected thread); the next chunk's
-// barrier is probed before the current chunk's MMAs are issued.
-__device__ __forceinline__ bool multiply(const Ctx& c, int tiles, const Queries& q, uint32_t& rit, uint32_t& slot,
-                                         uint32_t& phase, uint32_t& ait) {
+// The MMA warp's loop over one segment (the elected thread of rank 0); the
+// next chunk's barrier is probed before the current chunk's MMAs are issued.
+__device__ __forceinline__ bool multiply(const Ctx& c, int tiles, const Queries& q, uint32_t& rit, Ring& ring,
+                                         uint32_t& ait) {
   Bars* bars = c.bars;
-  const bool queries_stay = q.tiles == 1;
+  ring.mode(q.stay);
   const uint32_t full0 = bar_addr(bars->ring_full[0]), empty0 = bar_addr(bars->ring_empty[0]);
-  const uint64_t res0 = sw128_desc(c.base + kResOff, 16, 1024), ring0 = sw128_desc(c.base + kRingOff, 16, 1024);
+  const uint64_t res0 = sw128_desc(c.base + kResOff, 16, 1024);
+  const uint64_t ring0 = sw128_desc(c.base + ring_off(q.stay), 16, 1024);
+  const uint32_t res_step = (q.stay ? kHalf : kChunk) >> 4;
   auto wait_resident = [&]() {
     const bool ok = wait_phase(bar_addr(bars->res_full), rit & 1u, c.wc);
     ++rit;
     return ok;
   };
   bool ready = false;
-  if (queries_stay && !wait_resident()) return false;
+  if (q.stay && !wait_resident()) return false;
   for (int j = 0; j < tiles; ++j) {
-    if (!queries_stay && !wait_resident()) return false;
-    const int streams = queries_stay ? 1 : q.tiles;
+    if (!q.stay && !wait_resident()) return false;
+    const int streams = q.stay ? 1 : q.tiles;
     for (int i = 0; i < streams; ++i, ++ait) {
       const int buf = ait % kAcc;
-      // the last tile of a sequence may have fewer rows (a multiple of 16)
-      const uint32_t idesc = idesc_bf16(128, min(128, q.rows - 128 * i), false, false);
-      const uint32_t d = c.tmem + 128 * buf;
+      const uint32_t idesc = idesc_bf16(256, tile_rows(q, i), false, false);
+      const uint32_t d = c.tmem + 256 * buf;
       if (!wait_phase(bar_addr(bars->acc_empty[buf]), ((ait / kAcc) & 1u) ^ 1u, c.wc)) return false;
       tc_fence_after();
 #pragma unroll 1
       for (int ch = 0; ch < kChunks; ++ch) {
-        if (!ready && !wait_phase(full0 + 8 * slot, phase, c.wc)) return false;
-        const uint32_t s = slot;
-        if (++slot == kRing) {
-          slot = 0;
-          phase ^= 1u;
-        }
-        ready = mbar_test_wait(full0 + 8 * slot, phase);
-        const uint64_t res = res0 + static_cast<uint32_t>(ch) * (kChunk >> 4), str = ring0 + s * (kChunk >> 4);
-        const uint64_t a = queries_stay ? str : res, bq = queries_stay ? res : str;
+        if (!ready && !wait_phase(full0 + 8 * ring.slot, ring.phase(), c.wc)) return false;
+        const uint32_t s = ring.slot;
+        ring.next();
+        ready = mbar_test_wait(full0 + 8 * ring.slot, ring.phase());
+        const uint64_t res = res0 + static_cast<uint32_t>(ch) * res_step, str = ring0 + s * (kChunk >> 4);
+        const uint64_t a = q.stay ? str : res, bq = q.stay ? res : str;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) mma_ss(d, a + 2 * kk, bq + 2 * kk, idesc, (ch | kk) ? 1u : 0u);
-        mma_commit(empty0 + 8 * s);
+        for (int kk = 0; kk < 4; ++kk) pair_mma_ss(d, a + 2 * kk, bq + 2 * kk, idesc, (ch | kk) ? 1u : 0u);
+        pair_commit(empty0 + 8 * s, kBoth);
       }
-      mma_commit(bar_addr(bars->acc_full[buf]));
+      pair_commit(bar_addr(bars->acc_full[buf]), kBoth);
     }
-    if (!queries_stay) mma_commit(bar_addr(bars->res_empty));
+    if (!q.stay) pair_commit(bar_addr(bars->res_empty), kBoth);
   }
-  if (queries_stay) mma_commit(bar_addr(bars->res_empty));
+  if (q.stay) pair_commit(bar_addr(bars->res_empty), kBoth);
   return true;
 }
 
-// lse of the 128 rows of a query tile in base 2: lane l holds rows l, l + 32, l + 64, l + 96.
-__device__ __forceinline__ void load_lse(const WeighParams& p, const Queries& q, int i, int lane, float (&l)[4]) {
+// Writes a query tile's lse in base 2 (rows past the tile: +inf, whose
+// exponential is 0) to its buffer, 64 rows per epilogue warp.
+__device__ __forceinline__ void stage_lse(const Ctx& c, const Queries& q, int i, uint32_t lit, int quad) {
+  float* dst = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(c.bars) + kLseOff) + (lit & 1u) * kStreamRows;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int r = 128 * i + 32 * k + lane;
-    l[k] = r < q.rows ? p.lse[static_cast<size_t>(q.row0) + r] * kLog2e : INFINITY;
+  for (int k = 0; k < 2; ++k) {
+    const int at = 64 * quad + 32 * k + c.lane;
+    const int r = kStreamRows * i + at;
+    dst[at] = r < q.rows ? c.p->lse[static_cast<size_t>(q.row0) + r] * kLog2e : INFINITY;
   }
+  __syncwarp();
+  if (c.lane == 0) mbar_arrive(bar_addr(c.bars->lse_full[lit & 1u]));
 }
 
-__device__ __forceinline__ bool accumulate(const Ctx& c, const Segment& g, const Queries& q, uint32_t& ait) {
+__device__ __forceinline__ bool accumulate(const Ctx& c, const Segment& g, const Queries& q, uint32_t& ait,
+                                           uint32_t& lit) {
   const WeighParams& p = *c.p;
   Bars* bars = c.bars;
   const int quad = c.warp & 3;
-  const int row = quad * 32 + c.lane;  // TMEM lane: token of the tile
+  const int row = c.rank * 128 + quad * 32 + c.lane;  // token of the tile: TMEM lane of this CTA
   const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+  const uint32_t empty0 = map_to_rank(bar_addr(bars->acc_empty[0]), 0);
   const float sl2 = p.softmax_scale * kLog2e;
   const size_t S = size_t(p.max_blocks) * kBlock;
   const int len_off = g.len - (q.n - 1);  // query token j sees the first len_off + j rows
-  float l[4];
-  if (q.tiles == 1) load_lse(p, q, 0, c.lane, l);
-  for (int j = g.blk_lo; j < g.blk_hi; j += 2) {
+  const float* lse = nullptr;
+  // A buffer is written again two tiles on: by then every warp has arrived
+  // for the tile between, that is, has left this one.
+  auto next_lse = [&](int i) {
+    stage_lse(c, q, i, lit, quad);
+    if (!warp_wait(bar_addr(bars->lse_full[lit & 1u]), (lit >> 1) & 1u, c.wc)) return false;
+    lse = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(bars) + kLseOff) + (lit & 1u) * kStreamRows;
+    ++lit;
+    return true;
+  };
+  if (q.stay && q.tiles > 0 && !next_lse(0)) return false;
+  for (int j = g.blk_lo; j < g.blk_hi; j += kTileBlocks) {
     const int tok = j * kBlock + row;
-    const int last = min(j * kBlock + kTileTok, g.len) - 1;
+    const int last = min((j + kTileBlocks) * kBlock, g.len) - 1;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     for (int i = 0; i < q.tiles; ++i, ++ait) {
-      if (q.tiles > 1) load_lse(p, q, i, c.lane, l);
+      if (!q.stay && !next_lse(i)) return false;
       const int buf = ait % kAcc;
       if (!warp_wait(bar_addr(bars->acc_full[buf]), (ait / kAcc) & 1u, c.wc)) return false;
       tc_fence_after();
-      const int cols = min(128, q.rows - 128 * i);  // a multiple of 16
-      const uint32_t taddr = c.tmem + lane_off + 128 * buf;
+      const int cols = tile_rows(q, i);  // a multiple of 16
+      const uint32_t taddr = c.tmem + lane_off + 256 * buf;
       // whether the tile's first row, which sees least, sees the tile's last token
-      const bool seen = last < len_off + 128 * i / p.H;
+      const bool seen = last < len_off + kStreamRows * i / p.H;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kStreamRows / 32; ++k) {
         if (32 * k >= cols) break;
         uint32_t v[32];
         tmem_ld32(taddr + 32 * k, v);
         tmem_ld_wait();
         if (seen && 32 * k + 32 <= cols) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            sum[e & 3] += ex2_approx(fmaf(__uint_as_float(v[e]), sl2, -__shfl_sync(0xffffffffu, l[k], e)));
+          for (int e = 0; e < 32; e += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(lse + 32 * k + e);
+            sum[0] += ex2_approx(fmaf(__uint_as_float(v[e]), sl2, -l.x));
+            sum[1] += ex2_approx(fmaf(__uint_as_float(v[e + 1]), sl2, -l.y));
+            sum[2] += ex2_approx(fmaf(__uint_as_float(v[e + 2]), sl2, -l.z));
+            sum[3] += ex2_approx(fmaf(__uint_as_float(v[e + 3]), sl2, -l.w));
+          }
         } else {
           // 16 columns at a time belong to one query token (H is a multiple of 16)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const int c0 = 32 * k + 16 * half;
-            const bool in = c0 < cols && tok < len_off + (128 * i + c0) / p.H;
+            const bool in = c0 < cols && tok < len_off + (kStreamRows * i + c0) / p.H;
 #pragma unroll
             for (int e = 16 * half; e < 16 * half + 16; ++e) {
-              const float x = ex2_approx(fmaf(__uint_as_float(v[e]), sl2, -__shfl_sync(0xffffffffu, l[k], e)));
+              const float x = ex2_approx(fmaf(__uint_as_float(v[e]), sl2, -lse[32 * k + e]));
               if (in) sum[e & 3] += x;
             }
           }
@@ -251,7 +330,7 @@ __device__ __forceinline__ bool accumulate(const Ctx& c, const Segment& g, const
       }
       tc_fence_before();
       __syncwarp();
-      if (c.lane == 0) mbar_arrive(bar_addr(bars->acc_empty[buf]));
+      if (c.lane == 0) mbar_arrive_cluster_relaxed(empty0 + 8 * buf);  // the loads are in registers
     }
     if (tok < g.len && j + (row >> 6) < g.blk_hi) {
       const int id = p.block_table[size_t(g.b) * p.max_blocks + tok / kBlock];
@@ -265,16 +344,15 @@ __device__ __forceinline__ bool accumulate(const Ctx& c, const Segment& g, const
   return true;
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 weigh_sm100_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                    const WeighParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  Bars* bars = reinterpret_cast<Bars*>(smem_raw + (base - raw));
+  const uint32_t base = smem_u32(smem_raw);
+  Bars* bars = reinterpret_cast<Bars*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kRing; ++s) {
+    for (int s = 0; s < kRingMax; ++s) {
       mbar_init(bar_addr(bars->ring_full[s]), 1);
       mbar_init(bar_addr(bars->ring_empty[s]), 1);
     }
@@ -282,19 +360,21 @@ weigh_sm100_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     mbar_init(bar_addr(bars->res_empty), 1);
     for (int s = 0; s < kAcc; ++s) {
       mbar_init(bar_addr(bars->acc_full[s]), 1);
-      mbar_init(bar_addr(bars->acc_empty[s]), 4);  // lane 0 of every epilogue warp
+      mbar_init(bar_addr(bars->acc_empty[s]), 8);  // every epilogue warp of both CTAs
     }
+    mbar_init(bar_addr(bars->lse_full[0]), 4);
+    mbar_init(bar_addr(bars->lse_full[1]), 4);
     bars->abort = 0;
     fence_mbar_init();
     prefetch_tmap(&qmap);
     prefetch_tmap(&kmap);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&bars->tmem_base), kTmemCols);
-    tmem_relinquish();
+    pair_tmem_alloc(smem_u32(&bars->tmem_base), kTmemCols);
+    pair_tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();
   tc_fence_after();
   Ctx c;
   c.p = &p;
@@ -302,6 +382,7 @@ weigh_sm100_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
   c.bars = bars;
   c.tmem = bars->tmem_base;
   c.wc = WaitCtx{p.spin_limit, &g_weigh_err, &bars->abort};
+  c.rank = static_cast<int>(cluster_ctarank());
   c.warp = warp;
   c.lane = lane;
 
@@ -313,24 +394,30 @@ weigh_sm100_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     }
 
   SegWalker w;
-  w.init(p.seq_lens, p.B, p.max_blocks, gridDim.x, blockIdx.x);
+  w.init(p.seq_lens, p.B, p.max_blocks, gridDim.x / 2, blockIdx.x / 2);
+  // swizzled tiles need 1024-byte aligned shared memory
+  if ((base & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicOr(&g_weigh_err, kErrTimeout);
+    w.b = p.B;  // no segments
+  }
   Segment gs;
-  uint32_t rit = 0, fit = 0, ait = 0, slot = 0, phase = 0;
+  uint32_t rit = 0, ait = 0, lit = 0;
+  Ring ring;
   while (w.next(gs)) {
     const Segment g = gs;  // in registers, not behind the walker's reference
     const Queries q = queries_of(p, g.b);
     int ok = 1;
     if (warp == 0) {
-      if (q.tiles > 0 && lane == 0) ok = produce(c, &qmap, &kmap, g, q, rit, fit) ? 1 : 0;
+      if (q.tiles > 0 && lane == 0) ok = produce(c, &qmap, &kmap, g, q, rit, ring) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
     } else if (warp == 1) {
       // counters live in the elected thread, the same one every time
-      if (q.tiles > 0 && elect_one()) {
-        if (!multiply(c, (g.blk_hi - g.blk_lo + 1) / 2, q, rit, slot, phase, ait)) ok = 0;
+      if (q.tiles > 0 && c.rank == 0 && elect_one()) {
+        if (!multiply(c, (g.blk_hi - g.blk_lo + kTileBlocks - 1) / kTileBlocks, q, rit, ring, ait)) ok = 0;
       }
       ok = __all_sync(0xffffffffu, ok);
     } else {
-      ok = accumulate(c, g, q, ait) ? 1 : 0;
+      ok = accumulate(c, g, q, ait, lit) ? 1 : 0;
     }
     if (!ok) break;
   }
@@ -344,25 +431,35 @@ weigh_sm100_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     }
     __syncthreads();
   }
+  // neither CTA leaves while the other may still signal it or run MMAs on its memory
+  cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(c.tmem, kTmemCols);
+    pair_tmem_dealloc(c.tmem, kTmemCols);
   }
+  cluster_sync();
 }
 
 }  // namespace
 
-cudaError_t launch_weigh(const WeighParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap, int num_sms,
+cudaError_t launch_weigh(const WeighParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
                          cudaStream_t stream) {
-  static std::atomic<bool> attr_set[64];
+  static std::atomic<int> clusters[64];  // pairs that fit on the device at once, 0 = not known yet
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!attr_set[dev].load(std::memory_order_acquire)) {
+  int pairs = clusters[dev].load(std::memory_order_acquire);
+  if (pairs == 0) {
     cudaError_t e = cudaFuncSetAttribute(weigh_sm100_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
     if (e != cudaSuccess) return e;
-    attr_set[dev].store(true, std::memory_order_release);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    if ((e = cudaOccupancyMaxActiveClusters(&pairs, weigh_sm100_kernel, &cfg)) != cudaSuccess) return e;
+    if (pairs < 1) pairs = 1;
+    clusters[dev].store(pairs, std::memory_order_release);
   }
-  weigh_sm100_kernel<<<num_sms, kThreads, kSmem, stream>>>(qmap, kmap, p);
+  weigh_sm100_kernel<<<2 * pairs, kThreads, kSmem, stream>>>(qmap, kmap, p);
   return cudaGetLastError();
 }
 
