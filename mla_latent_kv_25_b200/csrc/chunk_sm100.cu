@@ -164,16 +164,12 @@ struct Walker {
   __device__ __forceinline__ void init(const ChunkParams& pp, int engine_) {
     p = &pp;
     engine = engine_;
-    nt = *pp.n_tiles;
     count = 0;
-    t = nt;
-    s = e = 0;
-    const long long total = pp.pre[nt];
-    const int P = engines_of(pp, total);
-    if (engine >= P) return;
-    s = range_start(engine, total, P);
-    e = range_start(engine + 1, total, P);
-    t = tile_of(pp.pre, nt, s);
+    const ChunkEngine r = pp.engines[engine_];
+    s = r.s;
+    e = r.e;
+    t = r.t;
+    nt = r.nt;
   }
 
   __device__ __forceinline__ bool next(Seg& g) {
@@ -626,18 +622,19 @@ __device__ __forceinline__ void value_fixup(const Ctx& c) {
       if (!warp_wait(bar_addr(c.bars->v_full[s]), (vit / kVSlots) & 1u, c.wc)) return;
       const int from = max(0, min(nv, all_see - j * kBlock));
       if (from < kBlock) {
-        uint8_t* st = c.gbase + v_slot_off(s);
-        const int rows = kBlock - from;
-        for (int idx = c.lane; idx < rows * 4 * 8; idx += 32) {
-          const int ch = idx / (rows * 8), rem = idx % (rows * 8);
-          const int row = from + rem / 8;
-          uint4* at = reinterpret_cast<uint4*>(st + ch * kBlkChunk + row * 128 + (rem % 8) * 16);
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (row < nv) {
-            v = *at;
-            v = make_uint4(finite_or_zero(v.x), finite_or_zero(v.y), finite_or_zero(v.z), finite_or_zero(v.w));
+        // eight lanes per 128-byte row of a chunk
+        uint8_t* st = c.gbase + v_slot_off(s) + (c.lane & 7) * 16;
+        for (int row = from + (c.lane >> 3); row < kBlock; row += 4) {
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            uint4* at = reinterpret_cast<uint4*>(st + ch * kBlkChunk + row * 128);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row < nv) {
+              v = *at;
+              v = make_uint4(finite_or_zero(v.x), finite_or_zero(v.y), finite_or_zero(v.z), finite_or_zero(v.w));
+            }
+            *at = v;
           }
-          *at = v;
         }
         fence_proxy_async_smem();
       }
@@ -751,6 +748,13 @@ __device__ __forceinline__ void value_mma(const Ctx& c) {
 // Latent column of TMEM column c: every MMA's N = 256 columns are 128 of each
 // CTA's half.
 __device__ __forceinline__ int latent_of(int c) { return 256 * ((c >> 7) & 1) + 128 * (c >> 8) + (c & 127); }
+
+// A piece's output is kept by columns, four floats of one row next to those of
+// the next row ([slot][512 / 4][256 rows][4]): a warp, whose lanes are rows,
+// then stores 512 contiguous bytes at a time, and the merge reads so too.
+__device__ __forceinline__ size_t piece_unit(int slot, int col4, int row) {
+  return (size_t(slot) * (kDc / 4) + col4) * kTileRows + row;
+}
 
 // Writes 64 bytes of each of the warp's 32 rows (lane = row, v = its bytes):
 // turned around in shared memory, so that a store of the warp fills eight
@@ -867,21 +871,12 @@ __device__ __forceinline__ void value_epilogue(const Ctx& c) {
           uint32_t v[32];
           tmem_ld32(c.tmem + lane_off + ocol + 32 * ch, v);
           tmem_ld_wait();
-          const int col = latent_of(ocol + 32 * ch);
+          if (!live) continue;
+          float4* dst = reinterpret_cast<float4*>(p.o_part) + piece_unit(g.slot, latent_of(ocol + 32 * ch) / 4, row);
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            uint4 o[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int e = 16 * part + 4 * q;
-              o[q] = make_uint4(__float_as_uint(__uint_as_float(v[e]) * inv), __float_as_uint(__uint_as_float(v[e + 1]) * inv),
-                                __float_as_uint(__uint_as_float(v[e + 2]) * inv), __float_as_uint(__uint_as_float(v[e + 3]) * inv));
-            }
-            store_rows(stage, c.lane, o, [&](int r) -> uint8_t* {
-              if (row0 + r >= g.rows) return nullptr;
-              return reinterpret_cast<uint8_t*>(p.o_part + (size_t(g.slot) * kTileRows + row0 + r) * kDc + col + 16 * part);
-            });
-          }
+          for (int q = 0; q < 8; ++q)
+            dst[q * kTileRows] = make_float4(__uint_as_float(v[4 * q]) * inv, __uint_as_float(v[4 * q + 1]) * inv,
+                                             __uint_as_float(v[4 * q + 2]) * inv, __uint_as_float(v[4 * q + 3]) * inv);
         }
         tc_fence_before();
         __syncwarp();
@@ -1082,10 +1077,24 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
     if (t < nt) p.pre[t + 1] = blocks + incl;
     blocks += total;
   }
+  // every engine's range and first tile (t = nt: none)
+  __syncthreads();
+  const int P = engines_of(p, blocks);
+  for (int e = threadIdx.x; e < p.P; e += kPlanThreads) {
+    ChunkEngine r = {0, 0, nt, nt};
+    if (e < P) {
+      r.s = range_start(e, blocks, P);
+      r.e = range_start(e + 1, blocks, P);
+      r.t = tile_of(p.pre, nt, r.s);
+    }
+    p.engines[e] = r;
+  }
 }
 
-constexpr int kMergeRows = 8;  // one warp per row
-constexpr int kMergeThreads = 32 * kMergeRows;
+constexpr int kMergeWarps = 8;
+constexpr int kMergeThreads = 32 * kMergeWarps;
+constexpr int kMergeCols = 16;                                              // columns of a thread
+constexpr int kMergeGrid = (kTileRows / 32) * (kDc / kMergeCols) / kMergeWarps;  // CTAs per tile
 
 __device__ __forceinline__ void fill_row(const ChunkParams& p, size_t row, float lse, int lane) {
   uint4* dst = reinterpret_cast<uint4*>(p.out + row * kDc + lane * 16);
@@ -1094,101 +1103,77 @@ __device__ __forceinline__ void fill_row(const ChunkParams& p, size_t row, float
   if (lane == 0) p.lse[row] = lse;
 }
 
-// grid (engine boundaries, 256 / 8): the boundary at which a cut tile's first
-// piece ends merges that tile's rows:
+// grid (engines, kMergeGrid): the boundary at which a cut tile's first piece
+// ends merges that tile; a warp takes 32 rows (lane = row) and 16 columns:
 //   lse = M + log sum_i exp(lse_i - M),  out = sum_i exp(lse_i - lse) o_i.
 // Rows of tokens that see no cached token are written here, and after a
 // timeout every row of the call.
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int wrow = blockIdx.y * kMergeRows + (threadIdx.x >> 5);  // 0..255
+  const int wid = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);  // 0..255 within a tile
   const int nt = *p.n_tiles;
   if ((*reinterpret_cast<volatile uint32_t*>(p.err) & kErrTimeout) != 0) {
     for (int t = blockIdx.x; t < nt; t += gridDim.x)
-      if (wrow < p.tiles[t].y) fill_row(p, size_t(p.tiles[t].x) + wrow, NAN, lane);
+      for (int r = wid; r < p.tiles[t].y; r += kMergeGrid * kMergeWarps) fill_row(p, size_t(p.tiles[t].x) + r, NAN, lane);
     return;
   }
+  const long long total = p.pre[nt];
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     const int a = p.q_offsets[b], e = p.q_offsets[b + 1];
     if (a < 0 || e < a || e > p.T) continue;
     const int blind = e - a - checked_len(p.seq_lens, b, p.max_blocks, nullptr);  // tokens that see nothing
-    for (long long r = wrow; r < static_cast<long long>(blind) * p.H; r += kTileRows)
+    for (long long r = wid; r < static_cast<long long>(blind) * p.H; r += kMergeGrid * kMergeWarps)
       fill_row(p, size_t(a) * p.H + r, -INFINITY, lane);
   }
-  const long long total = p.pre[nt];
   const int P = engines_of(p, total);
   const int e1 = blockIdx.x + 1;  // the boundary between engines e1 - 1 and e1
   if (e1 >= P) return;
-  const long long x = range_start(e1, total, P);
-  const int t = tile_of(p.pre, nt, x);
+  const long long x = range_start(e1, total, P), s0 = range_start(e1 - 1, total, P);
+  const int t = p.engines[e1].t;
   const long long a = p.pre[t], z = p.pre[t + 1];
-  const long long s0 = range_start(e1 - 1, total, P);
   // merged at the boundary whose left engine holds the tile's first block
   if (x <= a + kTileUnits || s0 > a + kTileUnits) return;
   const int4 info = p.tiles[t];
-  if (wrow >= info.y) return;
+  const int row = (wid & 7) * 32 + lane, col4 = (wid >> 3) * (kMergeCols / 4);
+  if (row >= info.y) return;
   const int last = engine_of(z - 1, total, P);
   const int n = last - (e1 - 1) + 1;
   // the first piece is its engine's second segment if the engine's range starts in an earlier tile
   auto slot_of = [&](int i) { return 2 * (e1 - 1 + i) + (i == 0 && s0 < a ? 1 : 0); };
-  // 32 pieces at a time, one per lane
   float M = -INFINITY, sum = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    float v = -INFINITY;
-    if (i0 + lane < n) v = p.lse_part[size_t(slot_of(i0 + lane)) * kTileRows + wrow];
-    float m = v;
+  for (int i = 0; i < n; ++i) M = fmaxf(M, p.lse_part[size_t(slot_of(i)) * kTileRows + row]);
+  const float base = M == -INFINITY ? 0.f : M;
+  float acc[kMergeCols];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float Mn = fmaxf(M, m);
-    float e = Mn == -INFINITY ? 0.f : expf(v - Mn);  // NaN pieces make the sum NaN
-    if (v != v) e = v;
+  for (int k = 0; k < kMergeCols; ++k) acc[k] = 0.f;
+  // weights relative to M, divided by their sum at the end; an empty piece
+  // holds zeros and weighs exp(-inf) = 0, a NaN piece makes the row NaN
+#pragma unroll 2
+  for (int i = 0; i < n; ++i) {
+    const float wgt = expf(p.lse_part[size_t(slot_of(i)) * kTileRows + row] - base);
+    const float4* src = reinterpret_cast<const float4*>(p.o_part) + piece_unit(slot_of(i), col4, row);
+    sum += wgt;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
-    sum = (M == -INFINITY ? 0.f : sum * expf(M - Mn)) + e;
-    M = Mn;
-  }
-  const size_t row = size_t(info.x) + wrow;
-  if (M == -INFINITY && sum == 0.f) {
-    fill_row(p, row, -INFINITY, lane);
-    return;
-  }
-  const float L = M + logf(sum);
-  float acc[16];
-#pragma unroll
-  for (int k = 0; k < 16; ++k) acc[k] = 0.f;
-  // two pieces in flight; an empty piece holds zeros and weighs exp(-inf) = 0
-  for (int i = 0; i < n; i += 2) {
-    float wgt[2];
-    float4 v[2][4];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const size_t r = size_t(slot_of(min(i + u, n - 1))) * kTileRows + wrow;
-      wgt[u] = i + u < n ? expf(p.lse_part[r] - L) : 0.f;
-      const float4* src = reinterpret_cast<const float4*>(p.o_part + r * kDc + lane * 16);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) v[u][q] = src[q];
+    for (int q = 0; q < kMergeCols / 4; ++q) {
+      const float4 v = src[q * kTileRows];
+      acc[4 * q] += wgt * v.x;
+      acc[4 * q + 1] += wgt * v.y;
+      acc[4 * q + 2] += wgt * v.z;
+      acc[4 * q + 3] += wgt * v.w;
     }
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        acc[4 * q] += wgt[u] * v[u][q].x;
-        acc[4 * q + 1] += wgt[u] * v[u][q].y;
-        acc[4 * q + 2] += wgt[u] * v[u][q].z;
-        acc[4 * q + 3] += wgt[u] * v[u][q].w;
-      }
   }
-  uint32_t pk[8];
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint32_t pk[kMergeCols / 2];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    __nv_bfloat162 b2 = __floats2bfloat162_rn(acc[2 * k], acc[2 * k + 1]);
+  for (int k = 0; k < kMergeCols / 2; ++k) {
+    __nv_bfloat162 b2 = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
     pk[k] = *reinterpret_cast<uint32_t*>(&b2);
   }
-  uint4* dst = reinterpret_cast<uint4*>(p.out + row * kDc + lane * 16);
+  uint4* dst = reinterpret_cast<uint4*>(p.out + (size_t(info.x) + row) * kDc + 4 * col4);
   dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
   dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-  if (lane == 0) p.lse[row] = L;
+  if (col4 == 0) p.lse[size_t(info.x) + row] = sum == 0.f ? -INFINITY : M + logf(sum);
 }
 
 cudaError_t set_attributes() {
@@ -1230,7 +1215,7 @@ cudaError_t launch_chunk_sm100(const ChunkParams& p, const CUtensorMap& kmap, co
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   if (cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_sm100_kernel, kmap, qmap, p); e != cudaSuccess) return e;
-  cfg.gridDim = dim3(p.P, kTileRows / kMergeRows);
+  cfg.gridDim = dim3(p.P, kMergeGrid);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, chunk_merge_kernel, p);

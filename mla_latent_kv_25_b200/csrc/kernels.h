@@ -106,6 +106,13 @@ struct AppendRopeParams {
 };
 cudaError_t launch_cache_append_rope(const AppendRopeParams& p, cudaStream_t stream);
 
+// An engine's share of a chunk call: units [s, e) of the axis that is cut, the
+// first tile in it, and the number of tiles.
+struct __align__(8) ChunkEngine {
+  long long s, e;
+  int t, nt;
+};
+
 // Ragged chunks of query tokens over the paged cache (mla_chunk_attend).
 struct ChunkParams {
   const __nv_bfloat16* q;    // [T,H,576]
@@ -125,9 +132,10 @@ struct ChunkParams {
   int* n_tiles;        // tiles in the list
   int* tile_off;       // [B+1] first tile of each sequence
   int4* tiles;         // [max_tiles] (first row of q, rows, sequence, cached tokens seen by the last query token)
-  long long* pre;      // [max_tiles+1] cache blocks of the tiles before each
+  long long* pre;      // [max_tiles+1] units of the tiles before each
+  ChunkEngine* engines;  // [P]
   float* lse_part;     // [2P][256]
-  float* o_part;       // [2P][256][512]
+  float* o_part;       // [2P][512/4][256][4]
 };
 // Plan, attention and merge kernels.  kmap as for launch_weigh; qmap: q as
 // [T*H, 576] with 64 x 128 boxes.

@@ -73,7 +73,7 @@ constexpr int kChunkTileRows = 256;
 // engine).  A sequence of n tokens has ceil(n / (256 / H)) tiles.
 struct ChunkLayout {
   int max_tiles;
-  size_t n_tiles, tile_off, tiles, pre, lse_part, o_part, total;
+  size_t n_tiles, tile_off, tiles, pre, engines, lse_part, o_part, total;
 };
 
 inline ChunkLayout chunk_layout(int T, int B, int H, int P) {
@@ -83,7 +83,8 @@ inline ChunkLayout chunk_layout(int T, int B, int H, int P) {
   w.tile_off = 512;
   w.tiles = align256(w.tile_off + (size_t(B) + 1) * 4);
   w.pre = align256(w.tiles + size_t(w.max_tiles) * 16);
-  w.lse_part = align256(w.pre + (size_t(w.max_tiles) + 1) * 8);
+  w.engines = align256(w.pre + (size_t(w.max_tiles) + 1) * 8);
+  w.lse_part = align256(w.engines + size_t(P) * 24);
   w.o_part = align256(w.lse_part + size_t(2 * P) * kChunkTileRows * 4);
   w.total = align256(w.o_part + size_t(2 * P) * kChunkTileRows * kDc * 4);
   return w;
