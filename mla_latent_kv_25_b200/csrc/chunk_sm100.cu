@@ -104,8 +104,8 @@ __host__ __device__ constexpr uint32_t q_off(int ch) { return kQOff + ch * kQChu
 __host__ __device__ constexpr uint32_t k_slot_off(int s) { return kQOff + kChunks * kQChunk + s * kKSlot; }
 __host__ __device__ constexpr uint32_t v_slot_off(int s) { return 1024 + s * kVSlot; }
 __host__ __device__ constexpr uint32_t rec_off(int r) { return 1024 + kVSlots * kVSlot + r * kRecBytes; }
-// value: every epilogue warp's staging of 32 rows x 64 bytes of output
-constexpr uint32_t kStageBytes = 32 * 64;
+// value: every epilogue warp's staging of 16 rows x 128 bytes of output
+constexpr uint32_t kStageBytes = 16 * 128;
 __host__ __device__ constexpr uint32_t stage_off(int w) { return rec_off(kNP) + w * kStageBytes; }
 constexpr uint32_t kScoreSmem = k_slot_off(kKSlots);
 constexpr uint32_t kValueSmem = stage_off(8);
@@ -282,7 +282,7 @@ __device__ __forceinline__ void score_tma_k(const Ctx& c, const CUtensorMap* kma
       }
       for (int ch = 0; ch < kChunks; ++ch, ++fit) {
         const int s = fit % kKSlots;
-        if (!warp_wait(bar_addr(c.bars->k_empty[s]), ((fit / kKSlots) & 1u) ^ 1u, c.wc)) return;
+        if (!__all_sync(0xffffffffu, spin_phase(bar_addr(c.bars->k_empty[s]), ((fit / kKSlots) & 1u) ^ 1u, c.wc))) return;
         if (c.lane == 0) {
           // rank 0 announces the bytes of both CTAs; those of rank 1 may land first
           const uint32_t full = full0 + 8 * s;
@@ -343,7 +343,7 @@ __device__ __forceinline__ bool score_mma_segment(const Ctx& c, const Seg& g, ui
 #pragma unroll 1
     for (int ch = 0; ch < kChunks; ++ch) {
       if (first && !wait_phase(q_full0 + 8 * ch, seg & 1u, c.wc)) return false;
-      if (!ready && !wait_phase(k_full0 + 8 * slot, phase, c.wc)) return false;
+      if (!ready && !spin_phase(k_full0 + 8 * slot, phase, c.wc)) return false;
       const uint32_t s = slot;
       if (++slot == kKSlots) {
         slot = 0;
@@ -756,24 +756,31 @@ __device__ __forceinline__ size_t piece_unit(int slot, int col4, int row) {
   return (size_t(slot) * (kDc / 4) + col4) * kTileRows + row;
 }
 
-// Writes 64 bytes of each of the warp's 32 rows (lane = row, v = its bytes):
-// turned around in shared memory, so that a store of the warp fills eight
-// 64-byte pieces instead of touching 32 rows (measured: the output of a tile
-// 7.2 us when every lane stores its own row).  16-byte units are swizzled
+// Writes 128 bytes of each of the warp's 32 rows (lane = row, v = its bytes):
+// turned around in shared memory, 16 rows at a time, so that a store of the
+// warp fills four whole lines.  The time of a store goes with the lines it
+// touches (measured for a tile's output: 7 us when every lane stores its own
+// row, 2.3-5 us with eight 64-byte pieces a store).  16-byte units are swizzled
 // against bank conflicts.  dst(r) is row r's address, or null for a padding row.
 template <class Dst>
-__device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint4 (&v)[4], Dst dst) {
-  const int sw = (lane >> 1) & 3;
-  __syncwarp();
+__device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint4 (&a)[4], const uint4 (&b)[4], Dst dst) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ sw) << 4)) = v[q];
-  __syncwarp();
+  for (int half = 0; half < 2; ++half) {
+    __syncwarp();
+    if ((lane >> 4) == half) {
+      const int r = lane & 15;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 8 * i + (lane >> 2), q = lane & 3;
-    uint8_t* at = dst(r);
-    if (at != nullptr)
-      *reinterpret_cast<uint4*>(at + 16 * q) = *reinterpret_cast<const uint4*>(stage + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+      for (int q = 0; q < 8; ++q)
+        *reinterpret_cast<uint4*>(stage + r * 128 + ((q ^ (r & 7)) << 4)) = q < 4 ? a[q & 3] : b[q & 3];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 4 * i + (lane >> 3), q = lane & 7;
+      uint8_t* at = dst(16 * half + r);
+      if (at != nullptr)
+        *reinterpret_cast<uint4*>(at + 16 * q) = *reinterpret_cast<const uint4*>(stage + r * 128 + ((q ^ (r & 7)) << 4));
+    }
   }
 }
 
@@ -823,11 +830,13 @@ __device__ __forceinline__ void value_epilogue(const Ctx& c) {
       const float m_fin = meta.y, l_fin = meta.z;
       __syncwarp();
       if (c.lane == 0) mbar_arrive(bar_addr(c.bars->meta_done));
-      if (c.warp == 4) {
-        if (!warp_wait(bar_addr(c.bars->meta_done), nfinal & 1u, c.wc)) return;
+      // the record goes back to the score CTA once all eight warps have read it
+      auto release_record = [&]() {
+        if (c.warp != 4) return true;
+        if (!warp_wait(bar_addr(c.bars->meta_done), nfinal & 1u, c.wc)) return false;
         if (c.lane == 0) mbar_arrive_cluster_relaxed(pempty0 + 8 * (req & 0xffu));
-      }
-      ++nfinal;
+        return true;
+      };
       const bool live = row < g.rows;
       const float inv = l_fin > 0.f ? 1.f / l_fin : (l_fin == 0.f ? 0.f : l_fin);  // a NaN sum stays NaN
       const float lse = l_fin == 0.f ? -INFINITY : (m_fin + log2f(l_fin)) * 0.6931471805599453f;
@@ -857,15 +866,17 @@ __device__ __forceinline__ void value_epilogue(const Ctx& c) {
         tc_fence_before();
         __syncwarp();
         if (c.lane == 0) mbar_arrive_cluster_relaxed(o_free);
+        if (!release_record()) return;
 #pragma unroll
-        for (int ch = 0; ch < 8; ++ch) {
+        for (int ch = 0; ch < 8; ch += 2) {
           const int col = latent_of(ocol + 32 * ch);
-          store_rows(stage, c.lane, o[ch], [&](int r) -> uint8_t* {
+          store_rows(stage, c.lane, o[ch], o[ch + 1], [&](int r) -> uint8_t* {
             if (row0 + r >= g.rows) return nullptr;
             return reinterpret_cast<uint8_t*>(p.out + (size_t(g.row0) + row0 + r) * kDc + col);
           });
         }
       } else {
+        if (!release_record()) return;
 #pragma unroll 1
         for (int ch = 0; ch < 8; ++ch) {
           uint32_t v[32];
@@ -882,6 +893,7 @@ __device__ __forceinline__ void value_epilogue(const Ctx& c) {
         __syncwarp();
         if (c.lane == 0) mbar_arrive_cluster_relaxed(o_free);
       }
+      ++nfinal;
       if (live && half == 0) {
         if (g.slot < 0)
           p.lse[size_t(g.row0) + row] = lse;

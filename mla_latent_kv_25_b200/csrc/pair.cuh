@@ -62,6 +62,24 @@ __device__ __forceinline__ void pair_tma_load_2d(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+// Bounded wait that polls without sleeping, for the threads whose next step
+// feeds the tensor pipe (measured in the chunk kernel: 2 % of the call with
+// the K producer's sleeps gone, another 1.5 % with the MMA thread's).
+__device__ __forceinline__ bool spin_phase(uint32_t bar, uint32_t parity, const WaitCtx& w) {
+  const long long t0 = clock64();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_test_wait(bar, parity)) return true;
+    if ((i & 31u) == 0) {
+      if (*w.abort) return false;
+      if (clock64() - t0 > w.limit) {
+        atomicOr(w.err, kErrTimeout);
+        *w.abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
 // Arrive on a barrier of any CTA of the cluster (cluster address) without
 // releasing earlier writes: a release at cluster scope costs 0.5 us here
 // (measured: producers that arrived with one issued a 16 KB load per 0.6 us),
