@@ -463,6 +463,7 @@ size_t mla_evict_workspace_bytes(int B, int max_blocks_per_seq);
  * the blocks from ceil(n / 64) on are free for reuse.  No block may be in two rows of
  * the table, or twice in one, below the sequences' lengths (a shared prefix would be
  * compacted for all its sequences).
+ * max_blocks_per_seq: at most 65536 (MLA_ERR_UNSUPPORTED above).
  * workspace: mla_evict_workspace_bytes(...), 256-byte aligned, zero-filled before its
  * first use, one call at a time; error bits by mla_get_device_error (a row whose source
  * or destination has a bad block id is not moved).

@@ -696,7 +696,7 @@ mla_status_t mla_cache_weigh(const void* q, const int32_t* q_offsets, int T, con
 }
 
 size_t mla_evict_workspace_bytes(int B, int max_blocks_per_seq) {
-  if (B < 1 || B > kMaxBatch || !valid_table(max_blocks_per_seq)) return 0;
+  if (B < 1 || B > kMaxBatch || max_blocks_per_seq < 1 || max_blocks_per_seq > kMaxEvictBlocks) return 0;
   return evict_layout(B, max_blocks_per_seq).total;
 }
 
@@ -715,6 +715,7 @@ mla_status_t mla_cache_evict(const float* weight, const int32_t* slot_pos, const
       misaligned(keep, 4) || misaligned(block_table, 4) || misaligned(new_weight, 4) || misaligned(new_pos, 4) ||
       misaligned(new_lens, 4) || misaligned(workspace, 256))
     return MLA_ERR_INVALID_ARG;
+  if (max_blocks_per_seq > kMaxEvictBlocks) return MLA_ERR_UNSUPPORTED;
   const EvictLayout lay = evict_layout(B, max_blocks_per_seq);
   if (workspace_bytes < lay.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
   uint8_t* wsb = static_cast<uint8_t*>(workspace);

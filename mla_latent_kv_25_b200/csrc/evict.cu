@@ -8,19 +8,22 @@
 //
 // evict_select_kernel: one cluster of 1, 2, 4 or 8 CTAs per sequence, every
 //   CTA and in it every warp owning a contiguous range of slots.  The n-th
-//   largest weight is found by a radix select: four passes of 8 bits over an
-//   order-preserving integer image of the weights, which is formed once and
-//   stays in shared memory; the CTAs add up their histograms over distributed
-//   shared memory.  Ties, free slots and movers are ranked by ballots and
-//   prefix sums over warps and CTAs, so the lists are ordered and the result
-//   is the same every time.  Bound by the latency of its passes and barriers:
-//   16 bytes per slot are read and written.
+//   largest weight is found by a radix select: three passes (11, 11 and 10
+//   bits) over an order-preserving integer image of the weights, which is
+//   formed once and stays in shared memory; the CTAs add up their histograms
+//   over distributed shared memory.  Which slots stay is then one bit each;
+//   ties, free slots and movers are ranked by prefix sums of bit counts over
+//   words, warps and CTAs, so the lists are ordered and the result is the same
+//   every time.  Bound by the instructions of its passes (one SM per 16384
+//   slots of a long sequence) and by about eight cluster barriers of 1 us; 16
+//   bytes per slot are read and written.
 // evict_move_kernel: bulk copies of whole rows through shared memory, 64 rows
 //   in flight per warp.  Bound: HBM, 2304 bytes per moved row.
 #include <atomic>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "plan.h"
 #include "sm100.cuh"
 
 namespace mla {
@@ -31,8 +34,10 @@ using namespace sm100;
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
-// Slots of one CTA whose keys fit in shared memory (4 bytes and one bit each).
-constexpr int kKeysInShared = 49152;
+constexpr int kBins = 2048;
+// Slots of one CTA whose keys fit in shared memory (4 bytes and two bits each);
+// of a longer range only the bits are kept and the weights read in every pass.
+constexpr int kKeysInShared = 45056;
 
 // Order-preserving image of a weight: larger weight, larger key; -0 equals +0,
 // NaN ranks as -inf.
@@ -53,73 +58,160 @@ __device__ __forceinline__ int ld_cluster(uint32_t local, uint32_t rank) {
 }
 
 struct Shared {
-  int hist[4][2][256];   // per pass; the first pass has one histogram per class
-  int warp_val[kSelWarps];
-  int cta_val[6];        // published values: largest position, protected slots, ties, holes, movers
+  int hist[4][kBins];    // top digit of the unprotected and of the protected slots; second digit; third digit
+  int warp_val[2][kSelWarps];
+  int cta_val[6];        // published values: largest position, protected slots, ties, free slots, movers
   int pick[2];           // digit, rank within it
 };
 
-// Exclusive prefix of `mine` (one value per warp) over the block's warps.
-__device__ __forceinline__ int warps_before(Shared& sh, int warp, int lane, int mine, int* total) {
+// Exclusive prefixes of two values per warp over the block's warps, and their totals.
+__device__ __forceinline__ int2 warps_before(Shared& sh, int warp, int lane, int2 mine, int2* total) {
   __syncthreads();
-  if (lane == 0) sh.warp_val[warp] = mine;
+  if (lane == 0) {
+    sh.warp_val[0][warp] = mine.x;
+    sh.warp_val[1][warp] = mine.y;
+  }
   __syncthreads();
-  const int v = sh.warp_val[lane];
-  *total = warp_sum(v);
-  return warp_sum(lane < warp ? v : 0);
+  const int x = sh.warp_val[0][lane], y = sh.warp_val[1][lane];
+  *total = make_int2(warp_sum(x), warp_sum(y));
+  return make_int2(warp_sum(lane < warp ? x : 0), warp_sum(lane < warp ? y : 0));
 }
 
-// Publishes a value of this CTA and returns the sum over the CTAs before it
-// and over all.
 template <bool kCluster>
-__device__ __forceinline__ int ctas_before(Shared& sh, int what, int rank, int size, int mine, int* total) {
+__device__ __forceinline__ void everyone() {
+  if (kCluster)
+    cluster_sync();  // also releases and acquires the CTAs' global writes
+  else
+    __syncthreads();
+}
+
+// Publishes two values of this CTA (after the barrier others may read them)
+// and returns the sums over the CTAs before it and over all.
+template <bool kCluster>
+__device__ __forceinline__ int2 ctas_before(Shared& sh, int what, int rank, int size, int2 mine, int2* total) {
   if (!kCluster) {
     *total = mine;
-    return 0;
+    return make_int2(0, 0);
   }
-  if (threadIdx.x == 0) sh.cta_val[what] = mine;
+  if (threadIdx.x == 0) {
+    sh.cta_val[what] = mine.x;
+    sh.cta_val[what + 1] = mine.y;
+  }
   cluster_sync();
-  int before = 0, all = 0;
+  int2 before = make_int2(0, 0), all = make_int2(0, 0);
   for (int r = 0; r < size; ++r) {
-    const int v = ld_cluster(smem_u32(&sh.cta_val[what]), r);
-    all += v;
-    before += r < rank ? v : 0;
+    const int x = ld_cluster(smem_u32(&sh.cta_val[what]), r), y = ld_cluster(smem_u32(&sh.cta_val[what + 1]), r);
+    all.x += x;
+    all.y += y;
+    before.x += r < rank ? x : 0;
+    before.y += r < rank ? y : 0;
   }
   *total = all;
   return before;
 }
 
-// kStored: the keys and the protection bits live in shared memory.
+// The digit, from the largest down, at which the histogram summed over the
+// CTAs reaches `need`, and the rank left within it.  Every thread takes
+// kBins / kSelThreads digits.
+template <bool kCluster>
+__device__ __forceinline__ int2 find_digit(Shared& sh, const int* hist, int size, int need, int warp, int lane) {
+  constexpr int kEach = kBins / kSelThreads;
+  int c[kEach], sum = 0;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int digit = kBins - 1 - static_cast<int>(threadIdx.x) * kEach - k;
+    c[k] = 0;
+    if (kCluster) {
+      for (int r = 0; r < size; ++r) c[k] += ld_cluster(smem_u32(hist + digit), r);
+    } else {
+      c[k] = hist[digit];
+    }
+    sum += c[k];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  int2 total;
+  const int before0 = warps_before(sh, warp, lane, make_int2(__shfl_sync(0xffffffffu, incl, 31), 0), &total).x;
+  int before = before0 + incl - sum;
+  if (before < need && need <= before + sum) {
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      if (before < need && need <= before + c[k]) {
+        sh.pick[0] = kBins - 1 - static_cast<int>(threadIdx.x) * kEach - k;
+        sh.pick[1] = need - before;
+      }
+      before += c[k];
+    }
+  }
+  __syncthreads();
+  return make_int2(sh.pick[0], sh.pick[1]);
+}
+
+// Adds one to a bin per lane with bin >= 0; a warp whose lanes agree adds once.
+__device__ __forceinline__ void count_bins(int* hist, int bin, int lane) {
+  if (__all_sync(0xffffffffu, bin == __shfl_sync(0xffffffffu, bin, 0))) {
+    if (lane == 0 && bin >= 0) atomicAdd(hist + bin, 32);
+  } else if (bin >= 0) {
+    atomicAdd(hist + bin, 1);
+  }
+}
+
+// kStored: the keys live in shared memory.
 template <bool kCluster, bool kStored>
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const EvictParams p, int size, int room) {
   __shared__ Shared sh;
   extern __shared__ uint32_t dyn[];
-  uint32_t* keys = dyn;            // [room]
-  uint32_t* bits = dyn + room;     // [room / 32] protected slots
+  uint32_t* gbits = dyn;                // [room / 32] protected slots, later ties
+  uint32_t* kbits = gbits + room / 32;  // [room / 32] slots that stay
+  uint32_t* keys = kbits + room / 32;   // [room] if kStored
   const int b = static_cast<int>(blockIdx.x) / size;
   const int rank = kCluster ? static_cast<int>(cluster_ctarank()) : 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const size_t S = size_t(p.max_blocks) * kBlock;
   const float* w = p.weight + b * S;
   const int32_t* pos = p.slot_pos + b * S;
+  float* nw = p.new_weight + b * S;
+  int32_t* np = p.new_pos + b * S;
   const int L = checked_len(p.seq_lens, b, p.max_blocks, threadIdx.x == 0 && rank == 0 ? p.err : nullptr);
   const int n = min(max(p.keep[b], 0), L);
+  const int tid = rank * kSelThreads + threadIdx.x, threads = size * kSelThreads;
+  // the slots that stay, moved values and the freed tail are written at the end
+  auto copy_stays = [&]() {
+    if (nw != w || np != pos)
+      for (int s = tid; s < n; s += threads) {
+        nw[s] = w[s];
+        np[s] = pos[s];
+      }
+  };
+  if (n == L) {  // nothing to evict (the same decision in every CTA of the cluster)
+    everyone<kCluster>();  // new_lens may be seq_lens: all have read it
+    copy_stays();
+    if (threadIdx.x == 0 && rank == 0) {
+      p.n_moves[b] = 0;
+      p.new_lens[b] = n;
+    }
+    return;
+  }
   // this CTA's slots [c0, c1) and this warp's [lo, hi)
   const int share = ((L + size - 1) / size + 31) / 32 * 32;  // <= room
   const int c0 = min(L, rank * share), c1 = min(L, c0 + share);
   const int per = ((c1 - c0 + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
   const int lo = min(c1, c0 + warp * per), hi = min(c1, lo + per);
 
-  for (int i = threadIdx.x; i < 4 * 2 * 256; i += kSelThreads) (&sh.hist[0][0][0])[i] = 0;
+  for (int i = threadIdx.x; i < 4 * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
 
   // the newest position
   int last = INT32_MIN;
 #pragma unroll 4
   for (int s = lo + lane; s < hi; s += 32) last = max(last, pos[s]);
   last = warp_max(last);
-  if (lane == 0) sh.warp_val[warp] = last;
+  if (lane == 0) sh.warp_val[0][warp] = last;
   __syncthreads();
-  last = warp_max(sh.warp_val[lane]);
+  last = warp_max(sh.warp_val[0][lane]);
   if (kCluster) {
     if (threadIdx.x == 0) sh.cta_val[0] = last;
     cluster_sync();
@@ -129,7 +221,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
 
   // keys, protection bits, and the histogram of the top digit of each class
   int guarded_here = 0;
-#pragma unroll 2
+#pragma unroll 4
   for (int s0 = lo; s0 < hi; s0 += 32) {
     const int s = s0 + lane;
     const bool in = s < hi;
@@ -137,168 +229,129 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     const uint32_t key = in ? weight_key(w[s]) : 0u;
     const bool g = in && (ps < p.n_first || ps > from);
     const unsigned gm = __ballot_sync(0xffffffffu, g);
-    if (kStored) {
-      if (in) keys[s - c0] = key;
-      if (lane == 0) bits[(s0 - c0) >> 5] = gm;
-    }
+    if (kStored && in) keys[s - c0] = key;
+    if (lane == 0) gbits[(s0 - c0) >> 5] = gm;
     guarded_here += __popc(gm);
-    const int bin = in ? static_cast<int>((g ? 256u : 0u) | (key >> 24)) : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, bin);  // weights share few exponents
-    if (in && lane == __ffs(same) - 1) atomicAdd(&sh.hist[0][0][0] + bin, __popc(same));
+    count_bins(&sh.hist[0][0], in ? (g ? kBins : 0) + static_cast<int>(key >> 21) : -1, lane);
   }
-  int total, n_guarded;
-  warps_before(sh, warp, lane, guarded_here, &total);
-  ctas_before<kCluster>(sh, 1, rank, size, total, &n_guarded);
+  int2 here, all;
+  warps_before(sh, warp, lane, make_int2(guarded_here, 0), &here);
+  ctas_before<kCluster>(sh, 1, rank, size, here, &all);
+  const int n_guarded = all.x;
   // either some protected slots go too, or all stay and the others compete
   const bool among_guarded = n_guarded >= n;
   int need = among_guarded ? n : n - n_guarded;  // kept of the competing class
 
-  auto guarded = [&](int s) -> bool {
-    if (kStored) return (bits[(s - c0) >> 5] >> ((s - c0) & 31)) & 1u;
-    return pos[s] < p.n_first || pos[s] > from;
-  };
   auto key_of = [&](int s) -> uint32_t { return kStored ? keys[s - c0] : weight_key(w[s]); };
+  // bits of the competing class among the 32 slots from s0 on
+  auto competing = [&](int s0) -> uint32_t {
+    const uint32_t valid = hi - s0 >= 32 ? 0xffffffffu : (1u << (hi - s0)) - 1u;
+    const uint32_t g = gbits[(s0 - c0) >> 5];
+    return (among_guarded ? g : ~g) & valid;
+  };
 
   // radix select: the competing slots with key > thr are kept, and of those
   // with key == thr the first `need`.  need = 0 keeps none (thr = the largest key).
-  uint32_t thr = 0;
-  if (need == 0) {
-    thr = 0xffffffffu;
-  } else {
-    for (int pass = 0; pass < 4; ++pass) {
-      const int shift = 24 - 8 * pass;
-      int* hist = sh.hist[pass][pass == 0 && among_guarded ? 1 : 0];
-      if (pass > 0) {
-        for (int s0 = lo; s0 < hi; s0 += 32) {
-          const int s = s0 + lane;
-          if (s < hi) {
-            const uint32_t key = key_of(s);
-            if ((key >> (shift + 8)) == (thr >> (shift + 8)) && guarded(s) == among_guarded)
-              atomicAdd(&hist[(key >> shift) & 255u], 1);
-          }
-        }
-        if (kCluster)
-          cluster_sync();
-        else
-          __syncthreads();
-      }
-      if (warp == 0) {
-        // lane l holds digits 255-8l .. 248-8l, from the largest down
-        int c[8], sum = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int digit = 255 - 8 * lane - k;
-          c[k] = 0;
-          if (kCluster) {
-            for (int r = 0; r < size; ++r) c[k] += ld_cluster(smem_u32(&hist[digit]), r);
-          } else {
-            c[k] = hist[digit];
-          }
-          sum += c[k];
-        }
-        int incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += v;
-        }
-        int before = incl - sum;
-        if (before < need && need <= incl) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if (before < need && need <= before + c[k]) {
-              sh.pick[0] = 255 - 8 * lane - k;
-              sh.pick[1] = need - before;
-            }
-            before += c[k];
-          }
+  uint32_t thr = 0xffffffffu;
+  if (need > 0) {
+    int2 d = find_digit<kCluster>(sh, sh.hist[among_guarded ? 1 : 0], size, need, warp, lane);
+    thr = static_cast<uint32_t>(d.x);
+    for (int pass = 1; pass < 3; ++pass) {
+      const int shift = pass == 1 ? 10 : 0, width = pass == 1 ? 11 : 10;
+#pragma unroll 2
+      for (int s0 = lo; s0 < hi; s0 += 32) {
+        if ((competing(s0) >> lane) & 1u) {
+          const uint32_t key = key_of(s0 + lane);
+          if ((key >> (shift + width)) == thr) atomicAdd(&sh.hist[1 + pass][(key >> shift) & ((1u << width) - 1u)], 1);
         }
       }
-      __syncthreads();
-      thr |= static_cast<uint32_t>(sh.pick[0]) << shift;
-      need = sh.pick[1];
-      __syncthreads();
+      everyone<kCluster>();
+      d = find_digit<kCluster>(sh, sh.hist[1 + pass], size, d.y, warp, lane);
+      thr = (thr << width) | static_cast<uint32_t>(d.x);
     }
+    need = d.y;
   }
 
-  auto above = [&](int s, bool* tie) -> bool {
-    const bool g = guarded(s);
-    if (g != among_guarded) {
-      *tie = false;
-      return g;  // a protected slot while the others compete stays
-    }
-    const uint32_t key = key_of(s);
-    *tie = key == thr;
-    return key > thr;
-  };
-  int count = 0;
+  // ties into gbits, all others that stay into kbits
+  int ties = 0;
+#pragma unroll 2
   for (int s0 = lo; s0 < hi; s0 += 32) {
-    bool tie = false;
-    if (s0 + lane < hi) above(s0 + lane, &tie);
-    count += tie ? 1 : 0;
-  }
-  int ties0 = warps_before(sh, warp, lane, warp_sum(count), &total);
-  int all;
-  ties0 += ctas_before<kCluster>(sh, 2, rank, size, total, &all);
-  // kept flags, 32 slots at a time, in slot order
-  auto walk = [&](auto&& visit) {
-    int ties = ties0;
-    for (int s0 = lo; s0 < hi; s0 += 32) {
-      const int s = s0 + lane;
-      bool tie = false, kept = false;
-      if (s < hi) kept = above(s, &tie);
-      const unsigned m = __ballot_sync(0xffffffffu, tie);
-      if (tie) kept = ties + __popc(m & ((1u << lane) - 1u)) < need;
-      ties += __popc(m);
-      visit(s, s < hi, kept);
+    const uint32_t can = competing(s0), g = gbits[(s0 - c0) >> 5];
+    const uint32_t key = (can >> lane) & 1u ? key_of(s0 + lane) : 0u;
+    const uint32_t over = __ballot_sync(0xffffffffu, key > thr) & can;
+    const uint32_t tie = __ballot_sync(0xffffffffu, key == thr) & can;
+    __syncwarp();
+    if (lane == 0) {
+      kbits[(s0 - c0) >> 5] = among_guarded ? over : over | g;  // protected slots stay while the others compete
+      gbits[(s0 - c0) >> 5] = tie;
     }
-  };
+    ties += __popc(tie);
+  }
+  int2 before = warps_before(sh, warp, lane, make_int2(ties, 0), &here);
+  int tie0 = before.x + ctas_before<kCluster>(sh, 2, rank, size, here, &all).x;
+
+  // one word of 32 slots per lane: the first `need` ties stay too; then the
+  // free slots below n and the movers behind it
   int holes = 0, movers = 0;
-  walk([&](int s, bool in, bool kept) {
-    holes += (in && !kept && s < n) ? 1 : 0;
-    movers += (in && kept && s >= n) ? 1 : 0;
-  });
-  int n_moves;
-  int hole0 = warps_before(sh, warp, lane, warp_sum(holes), &total);
-  hole0 += ctas_before<kCluster>(sh, 3, rank, size, total, &all);
-  int mover0 = warps_before(sh, warp, lane, warp_sum(movers), &total);
-  mover0 += ctas_before<kCluster>(sh, 4, rank, size, total, &n_moves);
+  auto hole_bits = [&](int s0, uint32_t k) {  // of the slots [s0, s0 + 32)
+    const int below = min(min(n, hi) - s0, 32);
+    return below <= 0 ? 0u : ~k & (below == 32 ? 0xffffffffu : (1u << below) - 1u);
+  };
+  auto mover_bits = [&](int s0, uint32_t k) {
+    const int below = n - s0;
+    return below <= 0 ? k : below >= 32 ? 0u : k & ~((1u << below) - 1u);
+  };
+  for (int s0 = lo; s0 < hi; s0 += 1024) {
+    const int s = s0 + 32 * lane;
+    const bool in = s < hi;
+    const uint32_t tie = in ? gbits[(s - c0) >> 5] : 0u;
+    const int c = __popc(tie);
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (in) {
+      int room_left = need - (tie0 + incl - c);  // ties that still stay
+      uint32_t take = room_left >= c ? tie : 0u;
+      if (room_left > 0 && room_left < c)
+        for (uint32_t t = tie; room_left > 0; --room_left) {
+          take |= t & (0u - t);
+          t &= t - 1;
+        }
+      const uint32_t k = kbits[(s - c0) >> 5] | take;
+      kbits[(s - c0) >> 5] = k;
+      holes += __popc(hole_bits(s, k));
+      movers += __popc(mover_bits(s, k));
+    }
+    tie0 += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  before = warps_before(sh, warp, lane, make_int2(warp_sum(holes), warp_sum(movers)), &here);
+  const int2 others = ctas_before<kCluster>(sh, 4, rank, size, here, &all);
+  int hole0 = before.x + others.x, mover0 = before.y + others.y;
+  const int n_moves = all.y;
   int2* moves = p.moves + b * (S / 2);
-  walk([&](int s, bool in, bool kept) {
-    const bool hole = in && !kept && s < n, mover = in && kept && s >= n;
-    const unsigned mh = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
-    const unsigned below = (1u << lane) - 1u;
-    if (hole) moves[hole0 + __popc(mh & below)].y = s;
-    if (mover) moves[mover0 + __popc(mm & below)].x = s;
+  const uint32_t below_me = (1u << lane) - 1u;
+  for (int s0 = lo; s0 < hi; s0 += 32) {
+    const uint32_t k = kbits[(s0 - c0) >> 5];
+    const uint32_t mh = hole_bits(s0, k), mm = mover_bits(s0, k);
+    if ((mh >> lane) & 1u) moves[hole0 + __popc(mh & below_me)].y = s0 + lane;
+    if ((mm >> lane) & 1u) moves[mover0 + __popc(mm & below_me)].x = s0 + lane;
     hole0 += __popc(mh);
     mover0 += __popc(mm);
-  });
+  }
   if (threadIdx.x == 0 && rank == 0) p.n_moves[b] = n_moves;
 
-  // the small arrays: the slots that stay, the moved values (read before any
-  // freed slot is cleared: they may live in the same arrays), the freed tail
-  float* nw = p.new_weight + b * S;
-  int32_t* np = p.new_pos + b * S;
-  const int tid = rank * kSelThreads + threadIdx.x, threads = size * kSelThreads;
-  if (nw != w || np != pos)
-    for (int s = tid; s < n; s += threads) {
-      nw[s] = w[s];
-      np[s] = pos[s];
-    }
-  // a cluster barrier releases and acquires global writes of its CTAs too
-  if (kCluster)
-    cluster_sync();
-  else
-    __syncthreads();
+  copy_stays();
+  everyone<kCluster>();  // the lists are written
   for (int k = tid; k < n_moves; k += threads) {
     const int2 m = moves[k];
     nw[m.y] = w[m.x];
     np[m.y] = pos[m.x];
   }
-  if (kCluster)
-    cluster_sync();
-  else
-    __syncthreads();
+  // in place, the moved values are read before any freed slot is cleared
+  if (nw == w || np == pos) everyone<kCluster>();
   for (int s = n + tid; s < L; s += threads) {
     nw[s] = 0.f;
     np[s] = -1;
@@ -394,12 +447,16 @@ cudaError_t allow_shared(Kernel kernel, int bytes, std::atomic<bool> (&done)[64]
   return e;
 }
 
+constexpr int kMaxDyn = kKeysInShared * 4 + kKeysInShared / 4;
+static_assert(sizeof(Shared) + kMaxDyn <= 232448 - 1024, "shared memory budget");
+static_assert(kMaxCluster * (kMaxDyn * 4LL - 1024) >= kMaxEvictBlocks * static_cast<long long>(kBlock), "bits of the longest sequence");
+
 template <bool kCluster, bool kStored>
 cudaError_t launch_select(const EvictParams& p, int size, int room, cudaStream_t stream) {
-  const int smem = kStored ? room * 4 + room / 8 : 0;
+  const int smem = room / 4 + (kStored ? room * 4 : 0);
   auto kernel = evict_select_kernel<kCluster, kStored>;
   static std::atomic<bool> attr_set[64];
-  if (cudaError_t e = allow_shared(kernel, kKeysInShared * 4 + kKeysInShared / 8, attr_set); e != cudaSuccess) return e;
+  if (cudaError_t e = allow_shared(kernel, kMaxDyn, attr_set); e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.B * size);
   cfg.blockDim = dim3(kSelThreads);
@@ -411,7 +468,7 @@ cudaError_t launch_select(const EvictParams& p, int size, int room, cudaStream_t
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = kCluster ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, p, size, kStored ? room : 0);
+  return cudaLaunchKernelEx(&cfg, kernel, p, size, room);
 }
 
 }  // namespace
@@ -426,15 +483,15 @@ cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t stream)
   // four; 4 x 32768 81 with one, 48 with eight).
   int size = 1;
   while (size < kMaxCluster && S >= 16384 && S / (2 * size) >= 4096 && 2LL * size * p.B <= sms) size *= 2;
-  const long long room = ((S + size - 1) / size + 31) / 32 * 32;
+  // two bits per slot have to fit in any case (evict_layout bounds S)
+  while (size < kMaxCluster && (S + size - 1) / size > kMaxDyn * 4 - 1024) size *= 2;
+  const int room = static_cast<int>(((S + size - 1) / size + 31) / 32 * 32);
   const bool stored = room <= kKeysInShared;
   cudaError_t e;
   if (size > 1)
-    e = stored ? launch_select<true, true>(p, size, static_cast<int>(room), stream)
-               : launch_select<true, false>(p, size, 0, stream);
+    e = stored ? launch_select<true, true>(p, size, room, stream) : launch_select<true, false>(p, size, room, stream);
   else
-    e = stored ? launch_select<false, true>(p, size, static_cast<int>(room), stream)
-               : launch_select<false, false>(p, size, 0, stream);
+    e = stored ? launch_select<false, true>(p, size, room, stream) : launch_select<false, false>(p, size, room, stream);
   if (e != cudaSuccess) return e;
   static std::atomic<bool> attr_set[64];
   if ((e = allow_shared(evict_move_kernel, int(kMoveSmem), attr_set)) != cudaSuccess) return e;

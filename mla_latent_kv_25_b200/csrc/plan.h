@@ -93,6 +93,8 @@ inline ChunkLayout chunk_layout(int T, int B, int H, int P) {
 // Workspace of an eviction: error word, moves per sequence, move lists (at
 // most half of a sequence's slots are free below its budget and filled from
 // behind it).
+constexpr int kMaxEvictBlocks = 65536;  // table width: two bits per slot stay in one cluster's shared memory
+
 struct EvictLayout {
   size_t n_moves, moves, total;
 };

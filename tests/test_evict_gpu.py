@@ -89,6 +89,14 @@ def test_evict_a_long_sequence():
     Case([140001], [70001], seed=6, kind="ties").check(4, 128)
 
 
+@pytest.mark.parametrize("width", [300, 1100, 8000])
+def test_evict_in_wide_tables(width):
+    """The table's width, not the lengths, sets how a sequence is shared out: few CTAs, many,
+    and too wide for the keys to stay in shared memory."""
+    Case([700, 19000], [300, 9000], seed=21, kind="ties", width=width).check(4, 32)
+    Case([5000], [1], seed=22, width=width, shuffled_pos=True).check(0, 7, in_place=True)
+
+
 def test_evict_many_sequences():
     g = torch.Generator().manual_seed(7)
     lens = torch.randint(0, 200, (300,), generator=g).tolist()

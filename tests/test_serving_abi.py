@@ -80,6 +80,8 @@ def test_short_workspaces_are_refused():
     assert n >= 256 + 2 * 4 + 2 * 4 * 32 * 8 and call("mla_cache_evict", EVICT, wsb=n - 1) == SMALL
     assert binding.mla_chunk_workspace_bytes(4, 2, 24, 4) == 0
     assert binding.mla_chunk_workspace_bytes(-1, 2, 128, 4) == 0
+    assert call("mla_cache_evict", EVICT, mb=65537) == 2 and binding.mla_evict_workspace_bytes(1, 65537) == 0
+    assert binding.mla_evict_workspace_bytes(1, 65536) > 0
     assert binding.mla_evict_workspace_bytes(0, 4) == 0 and binding.mla_evict_workspace_bytes(1, 0) == 0
 
 
