@@ -8,8 +8,8 @@
 //
 // evict_select_kernel: one cluster of 1, 2, 4 or 8 CTAs per sequence, every
 //   CTA and in it every warp owning a contiguous range of slots.  The n-th
-//   largest weight is found by a radix select: three passes (11, 11 and 10
-//   bits) over an order-preserving integer image of the weights, which is
+//   largest weight is found by a radix select: four passes of 8 bits over an
+//   order-preserving integer image of the weights, which is
 //   formed once and stays in shared memory; the CTAs add up their histograms
 //   over distributed shared memory.  Which slots stay is then one bit each;
 //   ties, free slots and movers are ranked by prefix sums of bit counts over
@@ -33,8 +33,12 @@ using namespace sm100;
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+// 16 (which needs an opt-in) measured 96 us against 103 for 4 x 131072 slots, but
+// 138 against 100 for 8 x 65536, whose eight clusters then do not fit at once.
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 2048;
+constexpr int kDigit = 8;
+constexpr int kBins = 1 << kDigit;
+constexpr int kPasses = 32 / kDigit;
 // Slots of one CTA whose keys fit in shared memory (4 bytes and two bits each);
 // of a longer range only the bits are kept and the weights read in every pass.
 constexpr int kKeysInShared = 45056;
@@ -58,7 +62,7 @@ __device__ __forceinline__ int ld_cluster(uint32_t local, uint32_t rank) {
 }
 
 struct Shared {
-  int hist[4][kBins];    // top digit of the unprotected and of the protected slots; second digit; third digit
+  int hist[kPasses + 1][kBins];  // top digit of the unprotected and of the protected slots; the lower digits
   int warp_val[2][kSelWarps];
   int cta_val[6];        // published values: largest position, protected slots, ties, free slots, movers
   int pick[2];           // digit, rank within it
@@ -98,54 +102,52 @@ __device__ __forceinline__ int2 ctas_before(Shared& sh, int what, int rank, int 
     sh.cta_val[what + 1] = mine.y;
   }
   cluster_sync();
-  int2 before = make_int2(0, 0), all = make_int2(0, 0);
-  for (int r = 0; r < size; ++r) {
-    const int x = ld_cluster(smem_u32(&sh.cta_val[what]), r), y = ld_cluster(smem_u32(&sh.cta_val[what + 1]), r);
-    all.x += x;
-    all.y += y;
-    before.x += r < rank ? x : 0;
-    before.y += r < rank ? y : 0;
+  int2 before = make_int2(0, 0), all = make_int2(0, 0), v[kMaxCluster];
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r)  // all remote loads in flight at once
+    v[r] = r < size ? make_int2(ld_cluster(smem_u32(&sh.cta_val[what]), r), ld_cluster(smem_u32(&sh.cta_val[what + 1]), r))
+                    : make_int2(0, 0);
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) {
+    all.x += v[r].x;
+    all.y += v[r].y;
+    before.x += r < rank ? v[r].x : 0;
+    before.y += r < rank ? v[r].y : 0;
   }
   *total = all;
   return before;
 }
 
 // The digit, from the largest down, at which the histogram summed over the
-// CTAs reaches `need`, and the rank left within it.  Every thread takes
-// kBins / kSelThreads digits.
+// CTAs reaches `need`, and the rank left within it.  Thread t < kBins takes
+// digit kBins - 1 - t.
 template <bool kCluster>
 __device__ __forceinline__ int2 find_digit(Shared& sh, const int* hist, int size, int need, int warp, int lane) {
-  constexpr int kEach = kBins / kSelThreads;
-  int c[kEach], sum = 0;
-#pragma unroll
-  for (int k = 0; k < kEach; ++k) {
-    const int digit = kBins - 1 - static_cast<int>(threadIdx.x) * kEach - k;
-    c[k] = 0;
+  int c = 0;
+  if (threadIdx.x < kBins) {
+    const int* mine = hist + (kBins - 1 - static_cast<int>(threadIdx.x));
     if (kCluster) {
-      for (int r = 0; r < size; ++r) c[k] += ld_cluster(smem_u32(hist + digit), r);
+      int v[kMaxCluster];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)  // all remote loads in flight at once
+        v[r] = r < size ? ld_cluster(smem_u32(mine), r) : 0;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) c += v[r];
     } else {
-      c[k] = hist[digit];
+      c = *mine;
     }
-    sum += c[k];
   }
-  int incl = sum;
+  int incl = c;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
   int2 total;
-  const int before0 = warps_before(sh, warp, lane, make_int2(__shfl_sync(0xffffffffu, incl, 31), 0), &total).x;
-  int before = before0 + incl - sum;
-  if (before < need && need <= before + sum) {
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      if (before < need && need <= before + c[k]) {
-        sh.pick[0] = kBins - 1 - static_cast<int>(threadIdx.x) * kEach - k;
-        sh.pick[1] = need - before;
-      }
-      before += c[k];
-    }
+  const int before = warps_before(sh, warp, lane, make_int2(__shfl_sync(0xffffffffu, incl, 31), 0), &total).x + incl - c;
+  if (before < need && need <= before + c) {
+    sh.pick[0] = kBins - 1 - static_cast<int>(threadIdx.x);
+    sh.pick[1] = need - before;
   }
   __syncthreads();
   return make_int2(sh.pick[0], sh.pick[1]);
@@ -202,11 +204,11 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
   const int per = ((c1 - c0 + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
   const int lo = min(c1, c0 + warp * per), hi = min(c1, lo + per);
 
-  for (int i = threadIdx.x; i < 4 * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
+  for (int i = threadIdx.x; i < (kPasses + 1) * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
 
   // the newest position
   int last = INT32_MIN;
-#pragma unroll 4
+#pragma unroll 8
   for (int s = lo + lane; s < hi; s += 32) last = max(last, pos[s]);
   last = warp_max(last);
   if (lane == 0) sh.warp_val[0][warp] = last;
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
 
   // keys, protection bits, and the histogram of the top digit of each class
   int guarded_here = 0;
-#pragma unroll 4
+#pragma unroll 8
   for (int s0 = lo; s0 < hi; s0 += 32) {
     const int s = s0 + lane;
     const bool in = s < hi;
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     if (kStored && in) keys[s - c0] = key;
     if (lane == 0) gbits[(s0 - c0) >> 5] = gm;
     guarded_here += __popc(gm);
-    count_bins(&sh.hist[0][0], in ? (g ? kBins : 0) + static_cast<int>(key >> 21) : -1, lane);
+    count_bins(&sh.hist[0][0], in ? (g ? kBins : 0) + static_cast<int>(key >> (32 - kDigit)) : -1, lane);
   }
   int2 here, all;
   warps_before(sh, warp, lane, make_int2(guarded_here, 0), &here);
@@ -256,18 +258,18 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
   if (need > 0) {
     int2 d = find_digit<kCluster>(sh, sh.hist[among_guarded ? 1 : 0], size, need, warp, lane);
     thr = static_cast<uint32_t>(d.x);
-    for (int pass = 1; pass < 3; ++pass) {
-      const int shift = pass == 1 ? 10 : 0, width = pass == 1 ? 11 : 10;
-#pragma unroll 2
+    for (int pass = 1; pass < kPasses; ++pass) {
+      const int shift = 32 - kDigit * (pass + 1);
+#pragma unroll 4
       for (int s0 = lo; s0 < hi; s0 += 32) {
         if ((competing(s0) >> lane) & 1u) {
           const uint32_t key = key_of(s0 + lane);
-          if ((key >> (shift + width)) == thr) atomicAdd(&sh.hist[1 + pass][(key >> shift) & ((1u << width) - 1u)], 1);
+          if ((key >> (shift + kDigit)) == thr) atomicAdd(&sh.hist[1 + pass][(key >> shift) & (kBins - 1u)], 1);
         }
       }
       everyone<kCluster>();
       d = find_digit<kCluster>(sh, sh.hist[1 + pass], size, d.y, warp, lane);
-      thr = (thr << width) | static_cast<uint32_t>(d.x);
+      thr = (thr << kDigit) | static_cast<uint32_t>(d.x);
     }
     need = d.y;
   }
