@@ -397,6 +397,14 @@ mla_status_t mla_cache_append_rope(const void *c_kv, int ckv_ld, const void *k_r
 size_t mla_chunk_workspace_bytes(int T, int B, int H, int num_splits);
 
 /*
+ * mla_chunk_fp8_workspace_bytes - the same for an fp8 cache: rounded up to 256, plus the
+ * scratch block table and the widened bf16 copy of the blocks the batch reads, as in
+ * mla_decode_fp8_workspace_bytes.  Returns 0 on invalid arguments or when
+ * B * max_blocks_per_seq exceeds 2^24.
+ */
+size_t mla_chunk_fp8_workspace_bytes(int T, int B, int H, int max_blocks_per_seq, int num_splits);
+
+/*
  * mla_chunk_attend - attention of ragged chunks of new tokens over the paged latent
  * cache (prefill of a prompt in chunks, mixed batches): mla_decode_multi for any number
  * of tokens per sequence.  The queries of sequence b are tokens q_offsets[b] ..
@@ -406,14 +414,19 @@ size_t mla_chunk_workspace_bytes(int T, int B, int H, int num_splits);
  * q: bf16 [T,H,576]; q_offsets: int32 [B+1] on the device, non-decreasing, in 0..T;
  * out: bf16 [T,H,512]; lse: f32 [T,H].  Tokens before q_offsets[0] or at and past
  * q_offsets[B] are neither read nor written.  A token that sees no cached token gives
- * out = 0 and lse = -inf.  cache, block_table, seq_lens, softmax_scale, num_splits,
- * workspace (mla_chunk_workspace_bytes; 256-byte aligned, zero-filled before its first
- * use, one call at a time) and the error bits (mla_get_device_error) as for mla_decode,
- * bf16 cache; a sequence whose offsets decrease or leave 0..T records
- * MLA_DEVERR_SEQ_TOO_LONG and its tokens are not written.
+ * out = 0 and lse = -inf.  cache_dtype, cache, k_rope, block_scale, block_table,
+ * seq_lens, softmax_scale, num_splits, the error bits (mla_get_device_error) and the
+ * state after a timeout as for mla_decode; workspace as there too, of
+ * mla_chunk_workspace_bytes or, for an fp8 cache, mla_chunk_fp8_workspace_bytes bytes (the
+ * cache is widened to bf16 rows for the whole batch first; MLA_ERR_WORKSPACE_TOO_SMALL
+ * with less).  A sequence whose offsets decrease or leave 0..T records
+ * MLA_DEVERR_SEQ_TOO_LONG and its tokens are not written.  A cached row that is not finite
+ * affects the tokens that see it only.
  * T >= 0 (0 is a no-op), T * H <= 2^30.
  */
-mla_status_t mla_chunk_attend(const void *q, const int32_t *q_offsets, int T, const void *cache,
+mla_status_t mla_chunk_attend(const void *q, const int32_t *q_offsets, int T,
+                              mla_cache_dtype_t cache_dtype, const void *cache,
+                              const void *k_rope, const float *block_scale,
                               const int32_t *block_table, const int32_t *seq_lens, int B, int H,
                               int num_blocks, int max_blocks_per_seq, float softmax_scale,
                               void *out, float *lse, void *workspace, size_t workspace_bytes,
@@ -485,7 +498,7 @@ mla_status_t mla_cache_get_error(void *stream, uint32_t *err_bits);
 
 /*
  * mla_set_wait_limit - bound, in SM clock cycles, of every wait inside the
- * decode kernels launched from now on (process-wide; default about two
+ * decode, chunk, weight and eviction kernels launched from now on (process-wide; default about two
  * seconds of SM clock; cycles <= 0 restores the default).  Returns the
  * previous bound.  A wait that reaches the bound records MLA_DEVERR_TIMEOUT,
  * makes every role of the kernel leave its loop, lets copies in flight land

@@ -34,7 +34,7 @@ EXPORTS = ("mla_absorb_q", "mla_absorb_o", "mla_absorb_get_error", "mla_cache_ap
            "mla_decode_workspace_bytes", "mla_decode_fp8_workspace_bytes", "mla_decode",
            "mla_combine", "mla_get_device_error", "mla_status_string", "mla_num_sms",
            "mla_decode_noalloc", "mla_decode_noalloc_get_error", "mla_last_error_string",
-           "mla_rope_freqs", "mla_rope", "mla_cache_append_rope", "mla_chunk_workspace_bytes",
+           "mla_rope_freqs", "mla_rope", "mla_cache_append_rope", "mla_chunk_workspace_bytes", "mla_chunk_fp8_workspace_bytes",
            "mla_chunk_attend", "mla_cache_weigh", "mla_evict_workspace_bytes", "mla_cache_evict")
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 ROPE_LAYOUT = {"interleaved": 0x0, "half": 0x1}
@@ -113,9 +113,11 @@ def load():
                                             ctypes.c_uint, vp, i32, i32, i32, vp, vp, vp]
         L.mla_chunk_workspace_bytes.restype = u64
         L.mla_chunk_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.mla_chunk_fp8_workspace_bytes.restype = u64
+        L.mla_chunk_fp8_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
         L.mla_chunk_attend.restype = i32
-        L.mla_chunk_attend.argtypes = [vp, vp, i32, vp, vp, vp, i32, i32, i32, i32, ctypes.c_float,
-                                       vp, vp, vp, u64, i32, vp]
+        L.mla_chunk_attend.argtypes = [vp, vp, i32, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32,
+                                       ctypes.c_float, vp, vp, vp, u64, i32, vp]
         L.mla_cache_weigh.restype = i32
         L.mla_cache_weigh.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32,
                                       ctypes.c_float, vp, vp, vp]
@@ -461,11 +463,11 @@ def mla_cache_append_rope(c_kv, k_r, seq_idx, slot, pos, freqs, block_table, cac
     return cache
 
 
-def _need_paged(cache, block_table):
-    """Checks a bf16 paged cache and its table; returns (B, max_blocks, num_blocks)."""
-    _need(cache, "cache", torch.bfloat16)
-    if cache.dim() != 3 or tuple(cache.shape[1:]) != (64, 576):
-        raise ValueError("bf16 cache must be [num_blocks,64,576]")
+def _need_paged(cache, block_table, fp8=False):
+    """Checks a paged cache (bf16, or E4M3 codes) and its table; returns (B, max_blocks, num_blocks)."""
+    _need(cache, "cache", torch.uint8 if fp8 else torch.bfloat16)
+    if cache.dim() != 3 or tuple(cache.shape[1:]) != ((64, 512) if fp8 else (64, 576)):
+        raise ValueError("fp8 cache must be [num_blocks,64,512] uint8" if fp8 else "bf16 cache must be [num_blocks,64,576]")
     _need(block_table, "block_table", torch.int32)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B,max_blocks]")
@@ -476,38 +478,54 @@ def mla_chunk_workspace_bytes(T: int, B: int, H: int, num_splits: int = 0) -> in
     return int(load().mla_chunk_workspace_bytes(int(T), int(B), int(H), int(num_splits)))
 
 
-def alloc_chunk_workspace(T: int, B: int, H: int, num_splits: int = 0, device=None) -> torch.Tensor:
-    """Zero-filled device workspace of the size mla_chunk_attend needs."""
-    n = mla_chunk_workspace_bytes(T, B, H, num_splits)
+def mla_chunk_fp8_workspace_bytes(T: int, B: int, H: int, max_blocks: int, num_splits: int = 0) -> int:
+    return int(load().mla_chunk_fp8_workspace_bytes(int(T), int(B), int(H), int(max_blocks), int(num_splits)))
+
+
+def alloc_chunk_workspace(T: int, B: int, H: int, num_splits: int = 0, device=None,
+                          fp8_max_blocks: int | None = None) -> torch.Tensor:
+    """Zero-filled device workspace of the size mla_chunk_attend needs; with
+    ``fp8_max_blocks`` (the block table's width) also for an fp8 cache."""
+    if fp8_max_blocks is None:
+        n, fn = mla_chunk_workspace_bytes(T, B, H, num_splits), "mla_chunk_workspace_bytes"
+    else:
+        n, fn = mla_chunk_fp8_workspace_bytes(T, B, H, fp8_max_blocks, num_splits), "mla_chunk_fp8_workspace_bytes"
     if n == 0:
-        raise MLAError("mla_chunk_workspace_bytes", 1)
+        raise MLAError(fn, 1)
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 
-def _need_chunk(q, q_offsets, cache, block_table, seq_lens):
+def _need_chunk(q, q_offsets, cache, block_table, seq_lens, fp8=False):
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [T,H,576] tensor")
     T, H = int(q.shape[0]), int(q.shape[1])
     _need(q, "q", torch.bfloat16, (T, H, 576))
-    B, mb, NB = _need_paged(cache, block_table)
+    B, mb, NB = _need_paged(cache, block_table, fp8)
     _need(q_offsets, "q_offsets", torch.int32, (B + 1,))
     _need(seq_lens, "seq_lens", torch.int32, (B,))
     return T, H, B, mb, NB
 
 
 def mla_chunk_attend(q, q_offsets, cache, block_table, seq_lens, softmax_scale, out, lse, workspace, *,
-                     num_splits=0, stream=None):
+                     k_rope=None, block_scale=None, num_splits=0, stream=None):
     """Attention of ragged chunks of new tokens (q [T,H,576], sequence b owning
-    tokens q_offsets[b]..q_offsets[b+1]-1) over the paged bf16 cache."""
-    T, H, B, mb, NB = _need_chunk(q, q_offsets, cache, block_table, seq_lens)
+    tokens q_offsets[b]..q_offsets[b+1]-1) over the paged cache: bf16 rows, or
+    E4M3 codes (uint8) with k_rope and block_scale."""
+    fp8 = isinstance(cache, torch.Tensor) and cache.dtype == torch.uint8
+    T, H, B, mb, NB = _need_chunk(q, q_offsets, cache, block_table, seq_lens, fp8)
+    if fp8:
+        _need(k_rope, "k_rope", torch.bfloat16, (NB, 64, 64))
+        _need(block_scale, "block_scale", torch.float32, (NB,))
+    elif k_rope is not None or block_scale is not None:
+        raise ValueError("k_rope and block_scale belong to an fp8 cache")
     _need(out, "out", torch.bfloat16, (T, H, 512))
     _need(lse, "lse", torch.float32, (T, H))
     _need(workspace, "workspace", torch.uint8)
-    _same_device(q, q_offsets, cache, block_table, seq_lens, out, lse, workspace)
+    _same_device(q, q_offsets, cache, k_rope, block_scale, block_table, seq_lens, out, lse, workspace)
     _check("mla_chunk_attend", load().mla_chunk_attend(
-        _ptr(q), _ptr(q_offsets), T, _ptr(cache), _ptr(block_table), _ptr(seq_lens), B, H, NB, mb,
-        float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), int(workspace.numel()), int(num_splits),
-        _stream(stream)))
+        _ptr(q), _ptr(q_offsets), T, MLA_CACHE_FP8_E4M3 if fp8 else MLA_CACHE_BF16, _ptr(cache), _ptr(k_rope),
+        _ptr(block_scale), _ptr(block_table), _ptr(seq_lens), B, H, NB, mb, float(softmax_scale), _ptr(out), _ptr(lse),
+        _ptr(workspace), int(workspace.numel()), int(num_splits), _stream(stream)))
     return out, lse
 
 

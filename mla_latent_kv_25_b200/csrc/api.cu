@@ -609,22 +609,36 @@ size_t mla_chunk_workspace_bytes(int T, int B, int H, int num_splits) {
   return P < 1 ? 0 : chunk_layout(T, B, H, P).total;
 }
 
-mla_status_t mla_chunk_attend(const void* q, const int32_t* q_offsets, int T, const void* cache,
+size_t mla_chunk_fp8_workspace_bytes(int T, int B, int H, int max_blocks_per_seq, int num_splits) {
+  if (!valid_table(max_blocks_per_seq)) return 0;
+  const size_t base = mla_chunk_workspace_bytes(T, B, H, num_splits);
+  if (base == 0 || static_cast<long long>(B) * max_blocks_per_seq > kMaxWideBlocks) return 0;
+  return wide_layout(base, B, max_blocks_per_seq).total;
+}
+
+mla_status_t mla_chunk_attend(const void* q, const int32_t* q_offsets, int T, mla_cache_dtype_t cache_dtype,
+                              const void* cache, const void* k_rope, const float* block_scale,
                               const int32_t* block_table, const int32_t* seq_lens, int B, int H,
                               int num_blocks, int max_blocks_per_seq, float softmax_scale, void* out,
                               float* lse, void* workspace, size_t workspace_bytes, int num_splits,
                               void* stream) {
+  const bool fp8 = cache_dtype == MLA_CACHE_FP8_E4M3;
+  if (cache_dtype != MLA_CACHE_BF16 && !fp8) return MLA_ERR_INVALID_ARG;
   if (!valid_chunk(T, B, H) || num_blocks < 1 || !valid_table(max_blocks_per_seq)) return MLA_ERR_INVALID_ARG;
   if (num_splits < 0 || num_splits > kMaxSplits || !isfinite(softmax_scale)) return MLA_ERR_INVALID_ARG;
   if (T == 0) return MLA_OK;
   if (!q || !q_offsets || !cache || !block_table || !seq_lens || !out || !lse || !workspace) return MLA_ERR_INVALID_ARG;
+  if (fp8 != (k_rope != nullptr) || fp8 != (block_scale != nullptr)) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(k_rope) || misaligned(block_scale, 4)) return MLA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || misaligned(lse, 4) || misaligned(q_offsets, 4) ||
       misaligned(block_table, 4) || misaligned(seq_lens, 4) || misaligned(workspace, 256))
     return MLA_ERR_INVALID_ARG;
   const int P = resolve_chunk_engines(num_splits);
   if (P < 1) return fail_with("no streaming multiprocessor count for the current device");
   const ChunkLayout lay = chunk_layout(T, B, H, P);
-  if (workspace_bytes < lay.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  const WideLayout wide = wide_layout(lay.total, B, max_blocks_per_seq);
+  if (fp8 && static_cast<long long>(B) * max_blocks_per_seq > kMaxWideBlocks) return MLA_ERR_UNSUPPORTED;
+  if (workspace_bytes < (fp8 ? wide.total : lay.total)) return MLA_ERR_WORKSPACE_TOO_SMALL;
   ChunkParams p;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_offsets = q_offsets;
@@ -652,10 +666,25 @@ mla_status_t mla_chunk_attend(const void* q, const int32_t* q_offsets, int T, co
   p.engines = reinterpret_cast<ChunkEngine*>(wsb + lay.engines);
   p.lse_part = reinterpret_cast<float*>(wsb + lay.lse_part);
   p.o_part = reinterpret_cast<float*>(wsb + lay.o_part);
+  if (fp8) {
+    // the rows the batch reads as a bf16 cache in the workspace, which the
+    // attention then reads (every row serves many queries: widening it once
+    // costs little next to the products)
+    p.block_table = reinterpret_cast<int32_t*>(wsb + wide.table);
+    p.cache = reinterpret_cast<__nv_bfloat16*>(wsb + wide.cache);
+    p.num_blocks = static_cast<int>(static_cast<long long>(B) * max_blocks_per_seq);
+  }
   CUtensorMap qmap, kmap;
   if (!encode_rows_map(&qmap, q, uint64_t(T) * H) ||
-      !encode_bf16_map(&kmap, cache, uint64_t(num_blocks) * kBlock, kRow, kRow * 2))
+      !encode_bf16_map(&kmap, p.cache, uint64_t(p.num_blocks) * kBlock, kRow, kRow * 2))
     return fail_with("tensor map encoding failed");
+  if (fp8) {
+    const cudaError_t e = launch_fp8_widen(
+        static_cast<const uint8_t*>(cache), static_cast<const __nv_bfloat16*>(k_rope), block_scale, block_table,
+        seq_lens, B, max_blocks_per_seq, num_blocks, reinterpret_cast<int32_t*>(wsb + wide.table),
+        reinterpret_cast<__nv_bfloat16*>(wsb + wide.cache), p.err, device_sms(), static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
   return status_of(launch_chunk_sm100(p, kmap, qmap, static_cast<cudaStream_t>(stream)));
 }
 

@@ -111,6 +111,33 @@ def test_chunk_reports_bad_ids_lengths_and_offsets():
     assert err & binding.DEVERR_SEQ_TOO_LONG and bool(torch.isfinite(out[:2]).all()) and bool(out[2:].isnan().all())
 
 
+def test_chunk_over_an_fp8_cache():
+    """Codes and block scales: the definition on bf16(code * scale), the value the widened row holds."""
+    c = Chunk([5, 0, 40], [300, 64, 100], 48, seed=20, before=1, after=1)
+    NB = c.cache.shape[0]
+    codes = torch.zeros(NB, 64, 512, dtype=torch.uint8, device="cuda")
+    k_rope = torch.zeros(NB, 64, 64, dtype=torch.bfloat16, device="cuda")
+    scale = torch.zeros(NB, device="cuda")
+    binding.mla_cache_quantize_fp8(c.cache.cuda(), torch.arange(NB, dtype=torch.int32, device="cuda"), codes, k_rope, scale)
+    assert binding.mla_cache_get_error() == 0
+    lat = codes.cpu().view(torch.float8_e4m3fn).float() * scale.cpu()[:, None, None]
+    c.cache = torch.cat([lat.bfloat16(), k_rope.cpu()], -1)
+    q, offs, _, table, lens = c.cuda()
+    out = torch.full((c.T, c.H, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((c.T, c.H), float("nan"), device="cuda")
+    ws = binding.alloc_chunk_workspace(c.T, c.B, c.H, fp8_max_blocks=table.shape[1])
+    binding.mla_chunk_attend(q, offs, codes, table, lens, SCALE, out, lse, ws, k_rope=k_rope, block_scale=scale)
+    assert binding.mla_get_device_error(ws) == 0
+    check_attention(f64(out), f64(lse), *serving.chunk_attend(*c.np(), SCALE), 300, "fp8 cache")
+    with pytest.raises(binding.MLAError):
+        binding.mla_chunk_attend(q, offs, codes, table, lens, SCALE, out, lse, binding.alloc_chunk_workspace(c.T, c.B, c.H),
+                                 k_rope=k_rope, block_scale=scale)
+    bad = table.clone()
+    bad[2, 0] = -1
+    binding.mla_chunk_attend(q, offs, codes, bad, lens, SCALE, out, lse, ws, k_rope=k_rope, block_scale=scale)
+    assert binding.mla_get_device_error(ws) == binding.DEVERR_BAD_BLOCK
+
+
 def test_chunk_in_a_graph_and_on_another_stream():
     c = Chunk([6, 3], [300, 200], 64, seed=10)
     want, wlse, _ = attend(c)

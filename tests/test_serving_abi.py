@@ -22,7 +22,7 @@ ROPE = dict(x=G, x_ldt=8192, x_ldh=64, pos=G, freqs=G, m=1.0, flags=0, y=G, y_ld
             st=None)
 APPEND = dict(c=G, ckv_ld=576, k=G, kr_ld=576, seq=G, slot=G, pos=G, T=4, freqs=G, m=1.0, flags=0, table=G, B=2, mb=4,
               NB=8, cache=G, slot_pos=G, st=None)
-CHUNK = dict(q=G, offs=G, T=4, cache=G, table=G, lens=G, B=2, H=128, NB=8, mb=4, scale=0.1, out=G, lse=G, ws=G,
+CHUNK = dict(q=G, offs=G, T=4, kind=0, cache=G, k_rope=None, scales=None, table=G, lens=G, B=2, H=128, NB=8, mb=4, scale=0.1, out=G, lse=G, ws=G,
              wsb=1 << 40, splits=4, st=None)
 WEIGH = dict(q=G, offs=G, T=4, lse=G, cache=G, table=G, lens=G, B=2, H=128, NB=8, mb=4, scale=0.1, win=G, wout=G,
              st=None)
@@ -50,7 +50,9 @@ def test_append_refuses(change):
 
 @pytest.mark.parametrize("change", [
     dict(q=None), dict(offs=None), dict(cache=None), dict(table=None), dict(lens=None), dict(out=None), dict(lse=None),
-    dict(ws=None), dict(T=-1), dict(B=0), dict(H=8), dict(H=144), dict(H=40), dict(NB=0), dict(mb=0),
+    dict(ws=None), dict(kind=2), dict(k_rope=G), dict(scales=G), dict(kind=1), dict(kind=1, k_rope=G), dict(kind=1, scales=G),
+    dict(kind=1, k_rope=P(4104), scales=G), dict(kind=1, k_rope=G, scales=P(4098)),
+    dict(T=-1), dict(B=0), dict(H=8), dict(H=144), dict(H=40), dict(NB=0), dict(mb=0),
     dict(mb=(1 << 24) + 1), dict(scale=float("nan")), dict(scale=float("inf")), dict(splits=-1), dict(splits=4097),
     dict(T=(1 << 23) + 1), dict(q=P(4104)), dict(cache=P(4104)), dict(out=P(4104)), dict(lse=P(4098)), dict(ws=P(4224))])
 def test_chunk_refuses(change):
@@ -76,6 +78,11 @@ def test_evict_refuses(change):
 def test_short_workspaces_are_refused():
     n = binding.mla_chunk_workspace_bytes(4, 2, 128, 4)
     assert n > 0 and call("mla_chunk_attend", CHUNK, wsb=n - 1) == SMALL
+    n8 = binding.mla_chunk_fp8_workspace_bytes(4, 2, 128, 4, 4)
+    assert n8 == -(-(-(-n // 256) * 256 + 4 * 8) // 256) * 256 + 8 * 64 * 576 * 2
+    assert call("mla_chunk_attend", CHUNK, kind=1, k_rope=G, scales=G, wsb=n8 - 1) == SMALL
+    assert call("mla_chunk_attend", CHUNK, kind=1, k_rope=G, scales=G, B=4096, mb=8192) == 2   # 2^25 blocks to widen
+    assert binding.mla_chunk_fp8_workspace_bytes(4, 4096, 128, 8192, 4) == 0
     n = binding.mla_evict_workspace_bytes(2, 4)
     assert n >= 256 + 2 * 4 + 2 * 4 * 32 * 8 and call("mla_cache_evict", EVICT, wsb=n - 1) == SMALL
     assert binding.mla_chunk_workspace_bytes(4, 2, 24, 4) == 0
