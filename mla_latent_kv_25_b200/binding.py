@@ -56,6 +56,8 @@ def load():
     """Load libmla.so (building it in-tree with nvcc first if it is absent or
     stale).  Raises if it cannot be built or loaded."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -381,27 +383,38 @@ def mla_get_device_error(workspace, stream=None) -> int:
     return int(v.value)
 
 
-def _same_device(*tensors):
-    """All tensors on the current device (the C entry points launch there)."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensor on {t.device}, current device cuda:{dev}")
+# The calls below check their tensors in one expression each (a third of the
+# time of checking them one property at a time, which a small call would feel)
+# and look for the reason only when it fails.
+
+def _want(t, name, dtype, shape, dev):
+    """A contiguous tensor of this dtype and shape on the current device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.get_device() == dev and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        _need(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
-def _need_rows(t, name, dim, width=None):
-    """bf16 CUDA rows with a contiguous last axis; other strides are free."""
+def _want_rows(t, name, dim, width, dev):
+    """bf16 rows with a contiguous last axis on the current device; other strides are free."""
+    if isinstance(t, torch.Tensor) and t.dtype == torch.bfloat16 and t.get_device() == dev and t.dim() == dim:
+        if t.shape[-1] == width and (t.stride(-1) == 1 or width == 1 or t.numel() == 0):
+            return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != dim or (width is not None and t.shape[-1] != width):
-        raise ValueError(f"{name}: expected {dim} axes" + (f", the last of {width}" if width else "")
-                         + f", got {tuple(t.shape)}")
-    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last axis must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if t.dim() != dim or t.shape[-1] != width:
+        raise ValueError(f"{name}: expected {dim} axes, the last of {width}, got {tuple(t.shape)}")
+    raise ValueError(f"{name}: the last axis must be contiguous")
+
+
+def _raw(t):
+    return None if t is None else t.data_ptr()
 
 
 def _rope_flags(layout, inverse=False):
@@ -425,17 +438,20 @@ def mla_rope_freqs(rot=64, base=10000.0, scaling="none", factor=1.0, orig_len=40
 def mla_rope(x, pos, freqs, y, *, mscale=1.0, layout="interleaved", inverse=False, stream=None):
     """y[t,h] = x[t,h] rotated by pos[t] * freqs.  x, y: [T,H,rot] bf16 views whose
     last axis is contiguous (e.g. the last columns of longer rows); y may be x."""
-    _need_rows(x, "x", 3)
-    T, H, rot = (int(v) for v in x.shape)
-    _need_rows(y, "y", 3, rot)
+    dev = torch.cuda.current_device()
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError("x must be a [T,H,rot] tensor")
+    T, H, rot = x.shape
+    _want_rows(x, "x", 3, rot, dev)
+    _want_rows(y, "y", 3, rot, dev)
     if y.shape != x.shape:
         raise ValueError(f"y: expected shape {tuple(x.shape)}, got {tuple(y.shape)}")
-    _need(pos, "pos", torch.int32, (T,))
-    _need(freqs, "freqs", torch.float64, (rot // 2,))
-    _same_device(x, pos, freqs, y)
-    _check("mla_rope", load().mla_rope(_ptr(x), x.stride(0), x.stride(1), _ptr(pos), _ptr(freqs), float(mscale),
-                                       _rope_flags(layout, inverse), _ptr(y), y.stride(0), y.stride(1), T, H, rot,
-                                       _stream(stream)))
+    _want(pos, "pos", torch.int32, (T,), dev)
+    _want(freqs, "freqs", torch.float64, (rot // 2,), dev)
+    xt, xh, _ = x.stride()
+    yt, yh, _ = y.stride()
+    _check("mla_rope", load().mla_rope(x.data_ptr(), xt, xh, pos.data_ptr(), freqs.data_ptr(), float(mscale),
+                                       _rope_flags(layout, inverse), y.data_ptr(), yt, yh, T, H, rot, _stream(stream)))
     return y
 
 
@@ -443,35 +459,39 @@ def mla_cache_append_rope(c_kv, k_r, seq_idx, slot, pos, freqs, block_table, cac
                           mscale=1.0, layout="interleaved", stream=None):
     """Write [c_kv | rotated k_r] rows of new tokens into slots of the paged bf16
     cache, rotated at ``pos`` (which need not be the slot)."""
-    _need_rows(c_kv, "c_kv", 2, 512)
-    T = int(c_kv.shape[0])
-    _need_rows(k_r, "k_r", 2, 64)
-    if int(k_r.shape[0]) != T:
-        raise ValueError(f"k_r: expected {T} rows, got {int(k_r.shape[0])}")
-    for t, name in ((seq_idx, "seq_idx"), (slot, "slot"), (pos, "pos")):
-        _need(t, name, torch.int32, (T,))
-    _need(freqs, "freqs", torch.float64, (32,))
-    B, mb, NB = _need_paged(cache, block_table)
+    dev = torch.cuda.current_device()
+    _want_rows(c_kv, "c_kv", 2, 512, dev)
+    _want_rows(k_r, "k_r", 2, 64, dev)
+    T = c_kv.shape[0]
+    if k_r.shape[0] != T:
+        raise ValueError(f"k_r: expected {T} rows, got {k_r.shape[0]}")
+    _want(seq_idx, "seq_idx", torch.int32, (T,), dev)
+    _want(slot, "slot", torch.int32, (T,), dev)
+    _want(pos, "pos", torch.int32, (T,), dev)
+    _want(freqs, "freqs", torch.float64, (32,), dev)
+    B, mb, NB = _need_paged(cache, block_table, dev)
     if slot_pos is not None:
-        _need(slot_pos, "slot_pos", torch.int32, (B, 64 * mb))
-    _same_device(c_kv, k_r, seq_idx, slot, pos, freqs, block_table, cache, slot_pos)
-    ckv_ld = c_kv.stride(0) if T > 1 else max(512, c_kv.stride(0) // 8 * 8)
-    kr_ld = k_r.stride(0) if T > 1 else max(64, k_r.stride(0) // 2 * 2)
+        _want(slot_pos, "slot_pos", torch.int32, (B, 64 * mb), dev)
+    ckv_ld, kr_ld = c_kv.stride(0), k_r.stride(0)
+    if T <= 1:  # a stride that no second row uses
+        ckv_ld, kr_ld = 512, 64
     _check("mla_cache_append_rope", load().mla_cache_append_rope(
-        _ptr(c_kv), ckv_ld, _ptr(k_r), kr_ld, _ptr(seq_idx), _ptr(slot), _ptr(pos), T, _ptr(freqs), float(mscale),
-        _rope_flags(layout), _ptr(block_table), B, mb, NB, _ptr(cache), _ptr(slot_pos), _stream(stream)))
+        c_kv.data_ptr(), ckv_ld, k_r.data_ptr(), kr_ld, seq_idx.data_ptr(), slot.data_ptr(), pos.data_ptr(), T,
+        freqs.data_ptr(), float(mscale), _rope_flags(layout), block_table.data_ptr(), B, mb, NB, cache.data_ptr(),
+        _raw(slot_pos), _stream(stream)))
     return cache
 
 
-def _need_paged(cache, block_table, fp8=False):
+def _need_paged(cache, block_table, dev, fp8=False):
     """Checks a paged cache (bf16, or E4M3 codes) and its table; returns (B, max_blocks, num_blocks)."""
-    _need(cache, "cache", torch.uint8 if fp8 else torch.bfloat16)
-    if cache.dim() != 3 or tuple(cache.shape[1:]) != ((64, 512) if fp8 else (64, 576)):
+    _want(cache, "cache", torch.uint8 if fp8 else torch.bfloat16, None, dev)
+    if cache.dim() != 3 or cache.shape[1:] != ((64, 512) if fp8 else (64, 576)):
         raise ValueError("fp8 cache must be [num_blocks,64,512] uint8" if fp8 else "bf16 cache must be [num_blocks,64,576]")
-    _need(block_table, "block_table", torch.int32)
+    _want(block_table, "block_table", torch.int32, None, dev)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B,max_blocks]")
-    return int(block_table.shape[0]), int(block_table.shape[1]), int(cache.shape[0])
+    B, mb = block_table.shape
+    return B, mb, cache.shape[0]
 
 
 def mla_chunk_workspace_bytes(T: int, B: int, H: int, num_splits: int = 0) -> int:
@@ -495,14 +515,14 @@ def alloc_chunk_workspace(T: int, B: int, H: int, num_splits: int = 0, device=No
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 
-def _need_chunk(q, q_offsets, cache, block_table, seq_lens, fp8=False):
+def _need_chunk(q, q_offsets, cache, block_table, seq_lens, dev, fp8=False):
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [T,H,576] tensor")
-    T, H = int(q.shape[0]), int(q.shape[1])
-    _need(q, "q", torch.bfloat16, (T, H, 576))
-    B, mb, NB = _need_paged(cache, block_table, fp8)
-    _need(q_offsets, "q_offsets", torch.int32, (B + 1,))
-    _need(seq_lens, "seq_lens", torch.int32, (B,))
+    T, H, _ = q.shape
+    _want(q, "q", torch.bfloat16, (T, H, 576), dev)
+    B, mb, NB = _need_paged(cache, block_table, dev, fp8)
+    _want(q_offsets, "q_offsets", torch.int32, (B + 1,), dev)
+    _want(seq_lens, "seq_lens", torch.int32, (B,), dev)
     return T, H, B, mb, NB
 
 
@@ -511,21 +531,22 @@ def mla_chunk_attend(q, q_offsets, cache, block_table, seq_lens, softmax_scale, 
     """Attention of ragged chunks of new tokens (q [T,H,576], sequence b owning
     tokens q_offsets[b]..q_offsets[b+1]-1) over the paged cache: bf16 rows, or
     E4M3 codes (uint8) with k_rope and block_scale."""
+    dev = torch.cuda.current_device()
     fp8 = isinstance(cache, torch.Tensor) and cache.dtype == torch.uint8
-    T, H, B, mb, NB = _need_chunk(q, q_offsets, cache, block_table, seq_lens, fp8)
+    T, H, B, mb, NB = _need_chunk(q, q_offsets, cache, block_table, seq_lens, dev, fp8)
     if fp8:
-        _need(k_rope, "k_rope", torch.bfloat16, (NB, 64, 64))
-        _need(block_scale, "block_scale", torch.float32, (NB,))
+        _want(k_rope, "k_rope", torch.bfloat16, (NB, 64, 64), dev)
+        _want(block_scale, "block_scale", torch.float32, (NB,), dev)
     elif k_rope is not None or block_scale is not None:
         raise ValueError("k_rope and block_scale belong to an fp8 cache")
-    _need(out, "out", torch.bfloat16, (T, H, 512))
-    _need(lse, "lse", torch.float32, (T, H))
-    _need(workspace, "workspace", torch.uint8)
-    _same_device(q, q_offsets, cache, k_rope, block_scale, block_table, seq_lens, out, lse, workspace)
+    _want(out, "out", torch.bfloat16, (T, H, 512), dev)
+    _want(lse, "lse", torch.float32, (T, H), dev)
+    _want(workspace, "workspace", torch.uint8, None, dev)
     _check("mla_chunk_attend", load().mla_chunk_attend(
-        _ptr(q), _ptr(q_offsets), T, MLA_CACHE_FP8_E4M3 if fp8 else MLA_CACHE_BF16, _ptr(cache), _ptr(k_rope),
-        _ptr(block_scale), _ptr(block_table), _ptr(seq_lens), B, H, NB, mb, float(softmax_scale), _ptr(out), _ptr(lse),
-        _ptr(workspace), int(workspace.numel()), int(num_splits), _stream(stream)))
+        q.data_ptr(), q_offsets.data_ptr(), T, MLA_CACHE_FP8_E4M3 if fp8 else MLA_CACHE_BF16, cache.data_ptr(),
+        _raw(k_rope), _raw(block_scale), block_table.data_ptr(), seq_lens.data_ptr(), B, H, NB, mb,
+        float(softmax_scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), int(num_splits),
+        _stream(stream)))
     return out, lse
 
 
@@ -533,15 +554,15 @@ def mla_cache_weigh(q, q_offsets, lse, cache, block_table, seq_lens, softmax_sca
                     stream=None):
     """weight_out = weight (or 0 if None) + the attention probability every cached
     token received from the queries, summed over heads and tokens."""
-    T, H, B, mb, NB = _need_chunk(q, q_offsets, cache, block_table, seq_lens)
-    _need(lse, "lse", torch.float32, (T, H))
+    dev = torch.cuda.current_device()
+    T, H, B, mb, NB = _need_chunk(q, q_offsets, cache, block_table, seq_lens, dev)
+    _want(lse, "lse", torch.float32, (T, H), dev)
     if weight is not None:
-        _need(weight, "weight", torch.float32, (B, 64 * mb))
-    _need(weight_out, "weight_out", torch.float32, (B, 64 * mb))
-    _same_device(q, q_offsets, lse, cache, block_table, seq_lens, weight, weight_out)
+        _want(weight, "weight", torch.float32, (B, 64 * mb), dev)
+    _want(weight_out, "weight_out", torch.float32, (B, 64 * mb), dev)
     _check("mla_cache_weigh", load().mla_cache_weigh(
-        _ptr(q), _ptr(q_offsets), T, _ptr(lse), _ptr(cache), _ptr(block_table), _ptr(seq_lens), B, H, NB, mb,
-        float(softmax_scale), _ptr(weight), _ptr(weight_out), _stream(stream)))
+        q.data_ptr(), q_offsets.data_ptr(), T, lse.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
+        seq_lens.data_ptr(), B, H, NB, mb, float(softmax_scale), _raw(weight), weight_out.data_ptr(), _stream(stream)))
     return weight_out
 
 
@@ -561,19 +582,21 @@ def mla_cache_evict(weight, slot_pos, seq_lens, keep, n_first, n_recent, block_t
                     new_lens, workspace, *, stream=None):
     """Cut every sequence to its ``keep`` best tokens and compact the cache;
     new_weight, new_pos and new_lens may be the inputs themselves."""
-    B, mb, NB = _need_paged(cache, block_table)
-    for t, name in ((weight, "weight"), (new_weight, "new_weight")):
-        _need(t, name, torch.float32, (B, 64 * mb))
-    for t, name in ((slot_pos, "slot_pos"), (new_pos, "new_pos")):
-        _need(t, name, torch.int32, (B, 64 * mb))
-    for t, name in ((seq_lens, "seq_lens"), (keep, "keep"), (new_lens, "new_lens")):
-        _need(t, name, torch.int32, (B,))
-    _need(workspace, "workspace", torch.uint8)
-    _same_device(weight, slot_pos, seq_lens, keep, block_table, cache, new_weight, new_pos, new_lens, workspace)
+    dev = torch.cuda.current_device()
+    B, mb, NB = _need_paged(cache, block_table, dev)
+    S = (B, 64 * mb)
+    _want(weight, "weight", torch.float32, S, dev)
+    _want(new_weight, "new_weight", torch.float32, S, dev)
+    _want(slot_pos, "slot_pos", torch.int32, S, dev)
+    _want(new_pos, "new_pos", torch.int32, S, dev)
+    _want(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    _want(keep, "keep", torch.int32, (B,), dev)
+    _want(new_lens, "new_lens", torch.int32, (B,), dev)
+    _want(workspace, "workspace", torch.uint8, None, dev)
     _check("mla_cache_evict", load().mla_cache_evict(
-        _ptr(weight), _ptr(slot_pos), _ptr(seq_lens), _ptr(keep), int(n_first), int(n_recent), _ptr(block_table), B,
-        NB, mb, _ptr(cache), _ptr(new_weight), _ptr(new_pos), _ptr(new_lens), _ptr(workspace),
-        int(workspace.numel()), _stream(stream)))
+        weight.data_ptr(), slot_pos.data_ptr(), seq_lens.data_ptr(), keep.data_ptr(), int(n_first), int(n_recent),
+        block_table.data_ptr(), B, NB, mb, cache.data_ptr(), new_weight.data_ptr(), new_pos.data_ptr(),
+        new_lens.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(stream)))
     return new_lens, new_weight, new_pos
 
 
