@@ -1015,7 +1015,9 @@ chunk_sm100_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   cluster_sync();
 }
 
+// Threads of the plan: one CTA, fewer warps at its barriers for small calls.
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanFew = 128;
 
 // Inclusive scan of one value per thread over the block.
 template <class T>
@@ -1029,7 +1031,7 @@ __device__ T block_scan(T v, T* warp_sums, T* total) {
   __syncthreads();
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
-  T w = warp_sums[lane];
+  T w = lane < static_cast<int>(blockDim.x >> 5) ? warp_sums[lane] : T(0);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const T u = __shfl_up_sync(0xffffffffu, w, o);
@@ -1047,7 +1049,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   __shared__ int isums[32];
   const int per = kTileRows / p.H;
   int nt = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < p.B; b0 += blockDim.x) {
     const int b = b0 + threadIdx.x;
     int tiles = 0;
     if (b < p.B) {
@@ -1075,7 +1077,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   }
   __syncthreads();
   long long blocks = 0;
-  for (int t0 = 0; t0 < nt; t0 += kPlanThreads) {
+  for (int t0 = 0; t0 < nt; t0 += blockDim.x) {
     const int t = t0 + threadIdx.x;
     long long mine = 0;
     if (t < nt) {
@@ -1100,7 +1102,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   // every engine's range and first tile (t = nt: none)
   __syncthreads();
   const int P = engines_of(p, blocks);
-  for (int e = threadIdx.x; e < p.P; e += kPlanThreads) {
+  for (int e = threadIdx.x; e < p.P; e += blockDim.x) {
     ChunkEngine r = {0, 0, nt, nt};
     if (e < P) {
       r.s = range_start(e, blocks, P);
@@ -1222,7 +1224,8 @@ cudaError_t launch_chunk_sm100(const ChunkParams& p, const CUtensorMap& kmap, co
     if (cudaError_t e = set_attributes(); e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  chunk_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+  const int threads = p.B <= kPlanFew && p.max_tiles <= kPlanFew ? kPlanFew : kPlanThreads;
+  chunk_plan_kernel<<<1, threads, 0, stream>>>(p);
   if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
