@@ -97,6 +97,31 @@ def test_evict_in_wide_tables(width):
     Case([5000], [1], seed=22, width=width, shuffled_pos=True).check(0, 7, in_place=True)
 
 
+@pytest.mark.parametrize("first,recent", [(4, 32), (0, 10 ** 9)])
+@pytest.mark.parametrize("kind", ["random", "ties", "equal", "special", "close"])
+@pytest.mark.parametrize("width", [300, 8000])
+def test_evict_orders_in_wide_tables(width, kind, first, recent):
+    """Clusters with the keys kept (300 blocks) and read again (8000), in place: protected slots
+    that compete, ties cut between CTAs, moves whose weights follow with the rows."""
+    Case([5000, 19100], [2501, 9001], seed=31, kind=kind, width=width, shuffled_pos=True).check(first, recent, in_place=True)
+
+
+@pytest.mark.parametrize("weights_in_place", [False, True])
+def test_evict_with_one_array_in_place(weights_in_place):
+    c = Case([700, 64, 3001], [300, 64, 1500], seed=33, shuffled_pos=True)
+    w, p, ln, kp, tb, ca = [t.cuda() for t in (c.weight, c.pos, c.lens, c.keep, c.table, c.cache)]
+    nw, np_ = (w, torch.full_like(p, -3)) if weights_in_place else (torch.full_like(w, -3.0), p)
+    ws = binding.alloc_evict_workspace(3, tb.shape[1])
+    binding.mla_cache_evict(w, p, ln, kp, 4, 32, tb, ca, nw, np_, ln, ws)
+    assert binding.mla_get_device_error(ws) == 0
+    kept = serving.evict(c.weight.numpy(), c.pos.numpy(), c.lens.numpy(), c.keep.numpy(), 4, 32)
+    for b, slots in enumerate(kept):
+        n, L, s = len(slots), int(c.lens[b]), torch.from_numpy(slots)
+        assert int(ln[b]) == n
+        assert torch.equal(nw[b, :n].cpu(), c.weight[b][s]) and torch.equal(np_[b, :n].cpu(), c.pos[b][s])
+        assert bool((nw[b, n:L] == 0).all()) and bool((np_[b, n:L] == -1).all())
+
+
 def test_evict_many_sequences():
     g = torch.Generator().manual_seed(7)
     lens = torch.randint(0, 200, (300,), generator=g).tolist()
