@@ -153,6 +153,14 @@ bool encode_rows_map(CUtensorMap* map, const void* base, uint64_t rows) {
   return encode_bf16(map, base, 2, dims, strides, box);
 }
 
+// Cache rows as [chunk][row][64 columns], boxes of n chunks x 64 rows.
+bool encode_chunks_map(CUtensorMap* map, const void* base, uint64_t rows, uint32_t n) {
+  cuuint64_t dims[3] = {64, rows, uint64_t(kRow) / 64};
+  cuuint64_t strides[2] = {uint64_t(kRow) * 2, 128};
+  cuuint32_t box[3] = {64, 64, n};
+  return encode_bf16(map, base, 3, dims, strides, box);
+}
+
 constexpr int kMaxBatch = 1 << 20;
 constexpr long long kDefaultSpin = 4000000000LL;  // ~2 s of SM clock
 std::atomic<long long> g_decode_wait_limit{kDefaultSpin};  // set by mla_set_wait_limit
@@ -674,9 +682,11 @@ mla_status_t mla_chunk_attend(const void* q, const int32_t* q_offsets, int T, ml
     p.cache = reinterpret_cast<__nv_bfloat16*>(wsb + wide.cache);
     p.num_blocks = static_cast<int>(static_cast<long long>(B) * max_blocks_per_seq);
   }
-  CUtensorMap qmap, kmap;
-  if (!encode_rows_map(&qmap, q, uint64_t(T) * H) ||
-      !encode_bf16_map(&kmap, p.cache, uint64_t(p.num_blocks) * kBlock, kRow, kRow * 2))
+  ChunkMaps maps;
+  const uint64_t cache_rows = uint64_t(p.num_blocks) * kBlock;
+  if (!encode_rows_map(&maps.q, q, uint64_t(T) * H) ||
+      !encode_bf16_map(&maps.k, p.cache, cache_rows, kRow, kRow * 2) ||
+      !encode_chunks_map(&maps.k2, p.cache, cache_rows, 2) || !encode_chunks_map(&maps.k4, p.cache, cache_rows, 4))
     return fail_with("tensor map encoding failed");
   if (fp8) {
     const cudaError_t e = launch_fp8_widen(
@@ -685,7 +695,7 @@ mla_status_t mla_chunk_attend(const void* q, const int32_t* q_offsets, int T, ml
         reinterpret_cast<__nv_bfloat16*>(wsb + wide.cache), p.err, device_sms(), static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e);
   }
-  return status_of(launch_chunk_sm100(p, kmap, qmap, static_cast<cudaStream_t>(stream)));
+  return status_of(launch_chunk_sm100(p, maps, static_cast<cudaStream_t>(stream)));
 }
 
 mla_status_t mla_cache_weigh(const void* q, const int32_t* q_offsets, int T, const float* lse,

@@ -7,19 +7,22 @@
 // TMEM of two SMs:
 //
 //   score pair (ranks 0, 1)                     value pair (ranks 2, 3)
-//   S[256 x 256] = Q K^T, cta_group::2:         O[256 x 512] += P V, cta_group::2:
-//   each CTA holds 128 query rows in shared     each CTA holds P of 128 rows and half
-//   memory and half of the pass's 256 tokens;   of the latent columns of each block;
-//   S is double-buffered in TMEM                O fills TMEM
-//   w0 TMA of K, w2 TMA of Q, w1 MMA (rank 0)   w0 TMA of V, w1 MMA (rank 2), w2 zeroes
-//   w4-11 softmax of the CTA's 128 rows,        V rows past the length, w3 relays P's
-//         P by st.async to CTA rank + 2         arrival to rank 2, w4-11 rescale, output
+//   S[256 x 128] = Q K^T, cta_group::2:         O[256 x 512] += P V, cta_group::2:
+//   each CTA holds 128 query rows (eight of     each CTA holds P of 128 rows and half
+//   their nine chunks in TMEM) and one of the   of the latent columns of each block;
+//   pass's two blocks; S is double-buffered     O fills TMEM
+//   w0 feeds Q and K, w2 the last chunk of Q,   w0 feeds V, w1 MMA (rank 2), w2 zeroes
+//   w1 MMA (rank 0); w4-7 and w8-11 softmax     V rows past the length, w3 relays P's
+//   of every other pass, P by st.async to       arrival to rank 2, w4-11 rescale, output
+//   CTA rank + 2
 //
 // Bound: the tensor pipe, 2 * rows * tokens * (576 + 512) FLOPs.  Why this
 // shape: with 256 rows to a cached token a pair reads 576 bytes of K (512 of
 // V) per SM and token while its MMAs take 18 (16) cycles, 32 bytes per clock
-// and SM from L2; 128 rows on two SMs would need twice that.  M = 256, N = 256
-// is also the shape at which the pipe runs at its full rate.
+// and SM from L2; 128 rows on two SMs would need twice that.  Q in TMEM (M =
+// 256, N = 128 runs at the pipe's full rate with A there) leaves 208 KB for K:
+// a ring of 80 KB next to all of Q in shared memory, with S of N = 256, took 490
+// us for the 16 tokens below.
 //
 // The tiles' blocks (and a charge per tile) are laid end to end and cut into P
 // equal ranges, one per engine, so ragged batches balance and a few tokens over
@@ -31,12 +34,11 @@
 // bf16 operand of a tensor-core product) while its sum is taken unrounded.
 // Every wait is bounded (WaitCtx).
 //
-// Measured (B200, H = 128): 512 tokens over 16384 cached ones 1.58 ms = 1480
-// TFLOP/s (0.90 of the measured bf16 peak; 1.84 ms in a long run under the
-// power cap, at 1.6 GHz); 16 tokens over 131072 0.49 ms = 1190 TFLOP/s.  What
-// remains: 33 clusters of four use 132 of 148 SMs, and with five 16 KB chunks
-// of K in flight per SM next to the 144 KB of Q a pass takes 3.2 us against the
-// 2.5 us of its MMAs.
+// Measured (B200, H = 128): 16 tokens over 131072 0.44 ms = 1330 TFLOP/s (0.91
+// of what 132 SMs can reach at the measured bf16 peak); 512 tokens over 16384
+// 1.64 ms = 1400 TFLOP/s (up to 1.8 ms in a long run under the power cap, at 1.6
+// GHz).  What remains: 33 clusters of four use 132 of 148 SMs, the start and the
+// end of a tile (about eight blocks' time), and the merge.
 #include <cuda.h>
 #include <math.h>
 
@@ -55,15 +57,17 @@ using namespace sm100;
 
 constexpr int kThreads = 384;
 constexpr int kTileRows = kChunkTileRows;     // 256
-constexpr int kPassBlocks = 4;                // blocks per QK pass (N = 256)
+constexpr int kPassBlocks = 2;                // blocks per QK pass (N = 128), one from each score CTA
 constexpr int kChunks = kRow / 64;            // 64-column chunks of a row
-constexpr int kKSlots = 5;                    // score: ring of [128 tokens x 64] chunks
+constexpr int kQTmem = kChunks - 1;           // chunks of Q kept in TMEM; the last stays in shared memory
+constexpr int kKSlots = 13;                   // score: ring of two [64 tokens x 64] chunks of K, or one of Q
 constexpr int kVSlots = 4;                    // value: ring of [64 tokens x 256] half blocks
 constexpr int kNP = 4;                        // P records in flight (5 measured the same, 3 are 15 % slower)
 
 constexpr uint32_t kQChunk = 128 * 128;       // [128 rows x 64] bf16
 constexpr uint32_t kBlkChunk = 64 * 128;      // [64 tokens x 64] bf16
 constexpr uint32_t kKSlot = 2 * kBlkChunk;
+static_assert(kKSlot == kQChunk, "Q is staged in the ring");
 constexpr uint32_t kVSlot = 4 * kBlkChunk;
 constexpr uint32_t kPBytes = 128 * 64 * 2;    // P [128 rows x 64 tokens] bf16, 8 x 8 core matrices
 constexpr uint32_t kPCoreK = 128 * 16;        // bytes per 8-token column of core matrices
@@ -74,18 +78,21 @@ constexpr float kRescaleThreshold = 8.0f;     // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
 static_assert(kPBytes + kMetaBytes + kFlagBytes <= kRecBytes, "record layout");
 constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemQ = 256;              // score: S in columns 0-127 and 128-255, then 32 columns per chunk of Q
+static_assert(kTmemQ + 32 * kQTmem == kTmemCols, "TMEM of the score pair");
 constexpr uint16_t kScoreMask = 0x3, kValueMask = 0xc;
 
 // Barriers live at the same offsets in all four CTAs; "leader" ones are used
 // in rank 0 (score) or rank 2 (value) only.
 struct Barriers {
-  uint64_t k_full[kKSlots];                    // leader: both CTAs' K chunks landed
+  uint64_t k_full[kKSlots];                    // leader: both CTAs' chunks landed
   uint64_t k_empty[kKSlots];                   // commit to both
-  uint64_t q_full[kChunks];                    // leader
-  uint64_t q_empty[kChunks];                   // commit to both
+  uint64_t q_full;                             // leader: the last chunk of Q
+  uint64_t q_empty;                            // commit to both
   uint64_t s_full[2];                          // commit to both
-  uint64_t s_empty[2];                         // leader: all softmax warps of both
-  uint64_t xchg[4];                            // the two softmax threads of a row swap max / sum
+  uint64_t s_empty[2];                         // leader: the softmax warps of both that read this buffer
+  uint64_t m_set[2][4];                        // a warp of this half published its rows' maxima
+  uint64_t l_set[2][4];                        // and their sums, before a segment's last pass
   uint64_t p_empty[kNP];                       // score CTAs: record r of the value CTA is free
   uint64_t v_full[kVSlots];                    // this CTA's V landed
   uint64_t v_ready[kVSlots];                   // leader: both CTAs' V landed and cleaned
@@ -102,13 +109,10 @@ struct Barriers {
 };
 static_assert(sizeof(Barriers) <= 1024, "barrier block too large");
 
-constexpr uint32_t kXchgOff = 1024;            // score: float [2 buffers][2 halves][128]
-constexpr uint32_t kXchgBytes = 2 * 2 * 128 * 4;
-constexpr uint32_t kQOff = 3072;               // score: Q, nine chunks
-constexpr uint32_t kXchgEnd = kXchgOff + kXchgBytes;
-static_assert(kXchgEnd <= kQOff, "exchange buffers");
-__host__ __device__ constexpr uint32_t q_off(int ch) { return kQOff + ch * kQChunk; }
-__host__ __device__ constexpr uint32_t k_slot_off(int s) { return kQOff + kChunks * kQChunk + s * kKSlot; }
+constexpr uint32_t kMaxOff = 1024;             // score: float [2 halves][128] running maxima
+constexpr uint32_t kSumOff = kMaxOff + 1024;   // score: float [2 halves][128] sums
+constexpr uint32_t kQOff = 3072;               // score: the last chunk of Q
+__host__ __device__ constexpr uint32_t k_slot_off(int s) { return kQOff + kQChunk + s * kKSlot; }
 __host__ __device__ constexpr uint32_t v_slot_off(int s) { return 1024 + s * kVSlot; }
 __host__ __device__ constexpr uint32_t rec_off(int r) { return 1024 + kVSlots * kVSlot + r * kRecBytes; }
 // value: every epilogue warp's staging of 16 rows x 128 bytes of output
@@ -121,7 +125,7 @@ constexpr uint32_t kValueSmem = stage_off(8);
 constexpr uint32_t kSmemBytes = kScoreSmem > kValueSmem ? kScoreSmem : kValueSmem;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
-__host__ __device__ constexpr uint32_t idesc_qk(int per) { return idesc_bf16(256, 128 * per, false, false); }
+constexpr uint32_t kIdescQK = idesc_bf16(256, 128, false, false);
 constexpr uint32_t kIdescPV = idesc_bf16(256, 256, false, true);
 
 // ------------------------------------------------------------------ segments
@@ -242,127 +246,196 @@ __device__ __forceinline__ int block_rows(const ChunkParams& p, const Seg& g, Bl
   return ok ? nv : 0;
 }
 
-// Blocks of a pass that each CTA of the score pair loads: with up to two
-// blocks one each (N = 128), else two each (N = 256); block k of the pass is
-// S columns 64k..64k+63 either way.
-__device__ __forceinline__ int blocks_per_cta(int nb) { return nb > 2 ? 2 : 1; }
-
 // ------------------------------------------------------------------ score pair
 
-__device__ __forceinline__ void score_tma_k(const Ctx& c, const CUtensorMap* kmap) {
+// The ring carries each segment's first eight chunks of Q, one per slot, then
+// its passes' chunks of K, two per slot (a pass has nine, so a slot may hold
+// the last of one pass and the first of the next).  One elected thread runs
+// it: with whole-warp waits and loads issued by `lane == 0` a slot took 850
+// cycles against the 512 of its MMAs, and this warp bound the whole kernel; with
+// per-slot bookkeeping of passes and blocks in the one thread still 590 (of
+// which the load is 40: it runs next to the softmax warps' code), so that the
+// loops here are tight and a slot is one load of two chunks.
+__device__ __forceinline__ void score_feed(const Ctx& c, const CUtensorMap* kmap, const CUtensorMap* kmap2, const CUtensorMap* qmap) {
   const ChunkParams& p = *c.p;
   Walker w;
   w.init(p, c.engine);
   Seg g;
-  BlockCursor cur;
-  uint32_t fit = 0;
-  const uint32_t full0 = map_to_rank(bar_addr(c.bars->k_full[0]), 0);
-  if (c.lane == 0) prefetch_tmap(kmap);
+  uint32_t slot = 0, parity = 1;
+  const uint32_t full0 = map_to_rank(bar_addr(c.bars->k_full[0]), 0), empty0 = bar_addr(c.bars->k_empty[0]);
+  prefetch_tmap(kmap);
+  prefetch_tmap(kmap2);
+  prefetch_tmap(qmap);
+  // The slot is free; rank 0 announces the bytes of both CTAs (those of rank 1
+  // may land first).
+  auto open = [&](uint32_t bytes) {
+    if (!spin_phase(empty0 + 8 * slot, parity, c.wc)) return false;
+    if (c.rank == 0) mbar_arrive_expect_tx(bar_addr(c.bars->k_full[0]) + 8 * slot, 2 * bytes);
+    return true;
+  };
+  auto advance = [&]() {
+    if (++slot == kKSlots) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  };
+  // this CTA's block of the pass from j on: its own, or a masked copy of the
+  // pass's only block, so that neither CTA's ring runs ahead; ids are read a
+  // pair of passes early
+  auto fetch = [&](const Seg& sg, int j) {
+    if (j >= sg.blk_hi) return 0;
+    return p.block_table[size_t(sg.b) * p.max_blocks + (j + c.rank < sg.blk_hi ? j + c.rank : j)];
+  };
+  auto row_of = [&](const Seg& sg, int id, int j) {
+    const bool ok = id >= 0 && id < p.num_blocks;
+    if (!ok && j + c.rank < sg.blk_hi) atomicOr(p.err, kErrBadBlock);
+    return ok ? id * kBlock : 0;
+  };
+  // chunks ch, ch + 2, ch + 4 and ch + 6 of a pass with their successors
+  auto four = [&](int row, int ch) {
+#pragma unroll 1
+    for (int end = ch + 8; ch < end; ch += 2) {
+      if (!open(2 * kBlkChunk)) return false;
+      pair_tma_load_3d(c.base + k_slot_off(0) + slot * kKSlot, kmap2, row, ch, full0 + 8 * slot);
+      advance();
+    }
+    return true;
+  };
   bool more = w.next(g);
-  if (more) cur.reset(p, g, c.lane);
+  int id0 = 0, id1 = 0;
+  if (more) {
+    id0 = fetch(g, g.blk_lo);
+    id1 = fetch(g, g.blk_lo + kPassBlocks);
+  }
   while (more) {
+#pragma unroll 1
+    for (int ch = 0; ch < kQTmem; ++ch) {
+      if (!open(kQChunk)) return;
+      // rows past the tile belong to other tokens (or read as zeros): their
+      // scores are masked
+      pair_tma_load_2d(c.base + k_slot_off(0) + slot * kKSlot, qmap, 64 * ch, g.row0 + 128 * c.rank, full0 + 8 * slot);
+      advance();
+    }
     Seg gn = g;
-    BlockCursor cn = cur;
-    for (int j = g.blk_lo; j < g.blk_hi; j += kPassBlocks) {
-      if (j == g.blk_lo + kPassBlocks || j + kPassBlocks >= g.blk_hi) {
-        // the next segment's records, while the ring is full
-        if (j == g.blk_lo + kPassBlocks || g.blk_hi - g.blk_lo <= kPassBlocks) {
-          more = w.next(gn);
-          if (more) cn.reset(p, gn, c.lane);
+    int n0 = 0, n1 = 0;
+    // two passes fill nine slots, the middle one with a chunk of each
+    for (int j = g.blk_lo; j < g.blk_hi; j += 2 * kPassBlocks) {
+      const bool two = j + kPassBlocks < g.blk_hi;
+      const int row0 = row_of(g, id0, j), row1 = two ? row_of(g, id1, j + kPassBlocks) : 0;
+      id0 = fetch(g, j + 2 * kPassBlocks);
+      id1 = fetch(g, j + 3 * kPassBlocks);
+      if (!four(row0, 0)) return;
+      if (!open(two ? 2 * kBlkChunk : kBlkChunk)) return;
+      const uint32_t dst = c.base + k_slot_off(0) + slot * kKSlot;
+      pair_tma_load_2d(dst, kmap, 64 * (kChunks - 1), row0, full0 + 8 * slot);
+      if (two) pair_tma_load_2d(dst + kBlkChunk, kmap, 0, row1, full0 + 8 * slot);
+      advance();
+      if (two && !four(row1, 1)) return;
+      if (j == g.blk_lo) {  // the next segment's records, while the ring is full
+        more = w.next(gn);
+        if (more) {
+          n0 = fetch(gn, gn.blk_lo);
+          n1 = fetch(gn, gn.blk_lo + kPassBlocks);
         }
-      }
-      const int nb = min(kPassBlocks, g.blk_hi - j);
-      const int per = blocks_per_cta(nb);
-      int blk[2] = {0, 0};
-      // blocks this CTA loads: at least one (a masked copy of the pass's first
-      // block if none is its own), so that neither CTA's ring runs ahead
-      int mine = 1;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int kb = c.rank * per + k;
-        // every lane takes part in the cursor's shuffle
-        const int nv = block_rows(p, g, cur, kb < nb ? j + kb : j, c.lane, &blk[k]);
-        if (k < per && kb < nb) {
-          mine = k + 1;
-          if (nv == 0 && c.lane == 0) atomicOr(p.err, kErrBadBlock);
-        }
-      }
-      for (int ch = 0; ch < kChunks; ++ch, ++fit) {
-        const int s = fit % kKSlots;
-        if (!__all_sync(0xffffffffu, spin_phase(bar_addr(c.bars->k_empty[s]), ((fit / kKSlots) & 1u) ^ 1u, c.wc))) return;
-        if (c.lane == 0) {
-          // rank 0 announces the bytes of both CTAs; those of rank 1 may land first
-          const uint32_t full = full0 + 8 * s;
-          if (c.rank == 0)
-            mbar_arrive_expect_tx(bar_addr(c.bars->k_full[s]), static_cast<uint32_t>(max(nb, 2)) * kBlkChunk);
-          const uint32_t dst = c.base + k_slot_off(s);
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            if (k < mine) pair_tma_load_2d(dst + k * kBlkChunk, kmap, 64 * ch, blk[k] * kBlock, full);
-        }
-        __syncwarp();
       }
     }
     g = gn;
-    cur = cn;
+    id0 = n0;
+    id1 = n1;
   }
 }
 
+// The last chunk of Q.
 __device__ __forceinline__ void score_tma_q(const Ctx& c, const CUtensorMap* qmap) {
   const ChunkParams& p = *c.p;
   Walker w;
   w.init(p, c.engine);
   Seg g;
   uint32_t seg = 0;
-  const uint32_t full0 = map_to_rank(bar_addr(c.bars->q_full[0]), 0);
-  if (c.lane == 0) prefetch_tmap(qmap);
+  const uint32_t full = map_to_rank(bar_addr(c.bars->q_full), 0);
   while (w.next(g)) {
-    for (int ch = 0; ch < kChunks; ++ch) {
-      if (!warp_wait(bar_addr(c.bars->q_empty[ch]), (seg & 1u) ^ 1u, c.wc)) return;
-      if (c.lane == 0) {
-        if (c.rank == 0) mbar_arrive_expect_tx(bar_addr(c.bars->q_full[ch]), 2 * kQChunk);
-        // rows past the tile belong to other tokens (or read as zeros): their
-        // scores are masked
-        pair_tma_load_2d(c.base + q_off(ch), qmap, 64 * ch, g.row0 + 128 * c.rank, full0 + 8 * ch);
-      }
-      __syncwarp();
+    if (!warp_wait(bar_addr(c.bars->q_empty), (seg & 1u) ^ 1u, c.wc)) return;
+    if (c.lane == 0) {
+      if (c.rank == 0) mbar_arrive_expect_tx(bar_addr(c.bars->q_full), 2 * kQChunk);
+      pair_tma_load_2d(c.base + kQOff, qmap, 64 * kQTmem, g.row0 + 128 * c.rank, full);
     }
+    __syncwarp();
     ++seg;
   }
 }
 
-// The elected thread of rank 0.  The barrier of the next chunk is probed
-// before the current chunk's MMAs are issued: a probe behind them would wait
-// for their issue and leave the pipe idle meanwhile.
-__device__ __forceinline__ bool score_mma_segment(const Ctx& c, const Seg& g, uint32_t seg, uint32_t& slot, uint32_t& phase,
-                                  uint32_t& pit) {
-  Barriers* bars = c.bars;
-  const uint32_t k_full0 = bar_addr(bars->k_full[0]), k_empty0 = bar_addr(bars->k_empty[0]);
-  const uint32_t q_full0 = bar_addr(bars->q_full[0]), q_empty0 = bar_addr(bars->q_empty[0]);
-  const uint64_t q0 = sw128_desc(c.base + q_off(0), 16, 1024), k0 = sw128_desc(c.base + k_slot_off(0), 16, 1024);
-  bool ready = false;
-  for (int j = g.blk_lo; j < g.blk_hi; j += kPassBlocks, ++pit) {
-    const bool first = j == g.blk_lo, last = j + kPassBlocks >= g.blk_hi;
-    const uint32_t idesc = idesc_qk(blocks_per_cta(min(kPassBlocks, g.blk_hi - j)));
-    const uint32_t d = c.tmem + 256 * (pit & 1u);
-    if (!wait_phase(bar_addr(bars->s_empty[pit & 1u]), ((pit >> 1) & 1u) ^ 1u, c.wc)) return false;
-    tc_fence_after();
-#pragma unroll 1
-    for (int ch = 0; ch < kChunks; ++ch) {
-      if (first && !wait_phase(q_full0 + 8 * ch, seg & 1u, c.wc)) return false;
-      if (!ready && !spin_phase(k_full0 + 8 * slot, phase, c.wc)) return false;
-      const uint32_t s = slot;
-      if (++slot == kKSlots) {
-        slot = 0;
-        phase ^= 1u;
-      }
-      ready = mbar_test_wait(k_full0 + 8 * slot, phase);
-      const uint64_t qd = q0 + static_cast<uint32_t>(ch) * (kQChunk >> 4), kd = k0 + s * (kKSlot >> 4);
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) pair_mma_ss(d, qd + 2 * kk, kd + 2 * kk, idesc, (ch | kk) ? 1u : 0u);
-      pair_commit(k_empty0 + 8 * s, kScoreMask);
-      if (last) pair_commit(q_empty0 + 8 * ch, kScoreMask);
+// The elected thread of rank 0.  The barrier of the next slot is probed before
+// the current slot's last MMAs are issued: a probe behind them would wait for
+// their issue and leave the pipe idle meanwhile.
+struct Feed {
+  uint32_t full0, empty0;  // barriers of slot 0
+  uint64_t k0;             // descriptor of slot 0
+  uint32_t slot, phase;
+  bool ready;
+
+  __device__ __forceinline__ bool wait(const Ctx& c) {
+    return ready || spin_phase(full0 + 8 * slot, phase, c.wc);
+  }
+  __device__ __forceinline__ void next() {
+    if (++slot == kKSlots) {
+      slot = 0;
+      phase ^= 1u;
     }
+    ready = mbar_test_wait(full0 + 8 * slot, phase);
+  }
+};
+
+// One pass.  kOdd: its first chunk is the second one of a slot.
+template <bool kOdd>
+__device__ __forceinline__ bool score_mma_pass(const Ctx& c, Feed& f, uint32_t d, bool first, bool last, uint32_t seg) {
+  const uint32_t q = c.tmem + kTmemQ;
+  const uint64_t q8 = sw128_desc(c.base + kQOff, 16, 1024);
+#pragma unroll
+  for (int ch = 0; ch < kChunks; ++ch) {
+    const bool second = ((ch + kOdd) & 1) != 0;
+    if (!second && !f.wait(c)) return false;
+    const uint32_t s = f.slot;
+    const uint64_t kd = f.k0 + s * (kKSlot >> 4) + (second ? kBlkChunk >> 4 : 0);
+    const bool done = second || (ch == kChunks - 1 && last);
+    if (done) f.next();
+    if (ch < kQTmem) {
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        pair_mma_ts(d, q + 32 * ch + 8 * kk, kd + 2 * kk, kIdescQK, (ch | kk) ? 1u : 0u);
+    } else {
+      if (first && !spin_phase(bar_addr(c.bars->q_full), seg & 1u, c.wc)) return false;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) pair_mma_ss(d, q8 + 2 * kk, kd + 2 * kk, kIdescQK, 1u);
+      if (last) pair_commit(bar_addr(c.bars->q_empty), kScoreMask);
+    }
+    if (done) pair_commit(f.empty0 + 8 * s, kScoreMask);
+  }
+  return true;
+}
+
+__device__ __forceinline__ bool score_mma_segment(const Ctx& c, const Seg& g, uint32_t seg, Feed& f, uint32_t& pit) {
+  Barriers* bars = c.bars;
+  // Q moves to TMEM once the MMAs that read the last segment's have finished
+  if (pit > 0 && !spin_phase(bar_addr(bars->s_full[(pit - 1) & 1u]), ((pit - 1) >> 1) & 1u, c.wc)) return false;
+  tc_fence_after();
+#pragma unroll 1
+  for (int ch = 0; ch < kQTmem; ++ch) {
+    if (!f.wait(c)) return false;
+    const uint64_t qd = f.k0 + f.slot * (kKSlot >> 4);
+    const uint32_t s = f.slot, d = c.tmem + kTmemQ + 32 * ch;
+    f.next();
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) pair_cp_128x32b(d + 8 * kk, qd + 2 * kk);
+    pair_commit(f.empty0 + 8 * s, kScoreMask);
+  }
+  bool odd = false;
+  for (int j = g.blk_lo; j < g.blk_hi; j += kPassBlocks, ++pit, odd = !odd) {
+    const bool first = j == g.blk_lo, last = j + kPassBlocks >= g.blk_hi;
+    const uint32_t d = c.tmem + 128 * (pit & 1u);
+    if (!spin_phase(bar_addr(bars->s_empty[pit & 1u]), ((pit >> 1) & 1u) ^ 1u, c.wc)) return false;
+    tc_fence_after();
+    if (!(odd ? score_mma_pass<true>(c, f, d, first, last, seg) : score_mma_pass<false>(c, f, d, first, last, seg)))
+      return false;
     pair_commit(bar_addr(bars->s_full[pit & 1u]), kScoreMask);
   }
   return true;
@@ -373,29 +446,36 @@ __device__ __forceinline__ void score_mma(const Ctx& c) {
     Walker w;
     w.init(*c.p, c.engine);
     Seg g;
-    uint32_t slot = 0, phase = 0, pit = 0, seg = 0;
-    while (w.next(g) && score_mma_segment(c, g, seg, slot, phase, pit)) ++seg;
+    Feed f{bar_addr(c.bars->k_full[0]), bar_addr(c.bars->k_empty[0]), sw128_desc(c.base + k_slot_off(0), 16, 1024),
+           0u, 0u, false};
+    uint32_t pit = 0, seg = 0;
+    while (w.next(g) && score_mma_segment(c, g, seg, f, pit)) ++seg;
   }
   __syncwarp();
 }
 
-// Swap a float with the other softmax thread of the same row.
-__device__ __forceinline__ bool xchg(const Ctx& c, int q4, int half, int h, uint32_t& xit, float mine, float* other) {
-  float* buf = reinterpret_cast<float*>(c.gbase + kXchgOff) + (xit & 1u) * 256;
-  buf[half * 128 + h] = mine;
-  mbar_arrive(bar_addr(c.bars->xchg[q4]));
-  if (!warp_wait(bar_addr(c.bars->xchg[q4]), xit & 1u, c.wc)) return false;
-  *other = buf[(half ^ 1) * 128 + h];
-  ++xit;
-  return true;
+// Publish one float per row to the other half's warp of the same rows.
+__device__ __forceinline__ float ld_shared(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void publish(uint32_t bar, uint32_t at, float v, int lane) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
 }
 
+// Thread = row; the four warps of a half take every other pass, so that one
+// half's exponentials overlap the other's loads and waits.  The running
+// maximum passes from pass to pass through shared memory; each half sums its
+// own passes, and the segment's last pass joins the two sums.
 __device__ __forceinline__ void score_softmax(const Ctx& c) {
   const ChunkParams& p = *c.p;
-  const int q4 = c.warp & 3;           // TMEM lane quadrant
-  const int half = (c.warp - 4) >> 2;  // blocks half, half + 2 of each pass
-  const int h = q4 * 32 + c.lane;      // row of this CTA
-  const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+  const int q4 = c.warp & 3;                                  // TMEM lane quadrant
+  const uint32_t half = static_cast<uint32_t>(c.warp - 4) >> 2;  // S buffer, parity of its passes
+  const int h = q4 * 32 + c.lane;                             // row of this CTA
+  const uint32_t s_addr = c.tmem + (static_cast<uint32_t>(q4 * 32) << 16) + 128 * half;
   // a zero scale (uniform attention) runs as a tiny one, so that a masked
   // score (-inf) still gives exactly 0
   const float sl2 = p.softmax_scale != 0.f ? p.softmax_scale * kLog2e : 1e-30f;
@@ -404,14 +484,17 @@ __device__ __forceinline__ void score_softmax(const Ctx& c) {
   const uint32_t to = static_cast<uint32_t>(c.rank) + 2;
   const uint32_t rec0 = map_to_rank(c.base + rec_off(0), to);
   const uint32_t pfull0 = map_to_rank(bar_addr(c.bars->p_full[0]), to);
-  const uint32_t sempty0 = map_to_rank(bar_addr(c.bars->s_empty[0]), 0);
+  const uint32_t sempty = map_to_rank(bar_addr(c.bars->s_empty[half]), 0);
+  // this half's published values and its barriers
+  const uint32_t maxima = c.base + kMaxOff + 512 * half + 4 * h, sums = maxima + (kSumOff - kMaxOff);
+  const uint32_t m_set = bar_addr(c.bars->m_set[half][q4]), l_set = bar_addr(c.bars->l_set[half][q4]);
+  const uint32_t other = half ? 0u - 512u : 512u, other_bar = half ? 0u - 32u : 32u;
   Walker w;
   w.init(p, c.engine);
   Seg g;
   BlockCursor cur;
-  uint32_t it = 0, pit = 0, xit = 0;
-  bool alive = true;
-  while (alive && w.next(g)) {
+  uint32_t it = 0, pit = 0, joined = 0;
+  while (w.next(g)) {
     cur.reset(p, g, c.lane);
     // this row's query token sees the tile's length without its last
     // tokens' rows; padding rows see nothing
@@ -419,31 +502,28 @@ __device__ __forceinline__ void score_softmax(const Ctx& c) {
     const int row_len = row < g.rows ? g.len - (g.rows - 1 - row) / p.H : 0;
     float m_ref = -INFINITY, l = 0.f;
     for (int j0 = g.blk_lo; j0 < g.blk_hi; j0 += kPassBlocks, ++pit) {
-      const bool first_pass = (j0 == g.blk_lo);
       const int nb = min(kPassBlocks, g.blk_hi - j0);
+      if ((pit & 1u) != half) {
+        it += static_cast<uint32_t>(nb);
+        continue;
+      }
+      const bool first_pass = j0 == g.blk_lo, last_pass = j0 + kPassBlocks >= g.blk_hi;
       int nvr[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int kb = half + 2 * k;
         int blk;
-        const int nv = block_rows(p, g, cur, kb < nb ? j0 + kb : j0, c.lane, &blk);
-        nvr[k] = kb < nb ? max(0, min(nv, row_len - (j0 + kb) * kBlock)) : 0;
+        const int nv = block_rows(p, g, cur, k < nb ? j0 + k : j0, c.lane, &blk);
+        nvr[k] = k < nb ? max(0, min(nv, row_len - (j0 + k) * kBlock)) : 0;
       }
-      const uint32_t buf = pit & 1u;
-      if (!warp_wait(bar_addr(c.bars->s_full[buf]), (pit >> 1) & 1u, c.wc)) {
-        alive = false;
-        break;
-      }
+      if (!warp_wait(bar_addr(c.bars->s_full[half]), (pit >> 1) & 1u, c.wc)) return;
       tc_fence_after();
       uint32_t sv[128];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        tmem_ld32(c.tmem + lane_off + 256 * buf + 64 * half + 128 * (q >> 1) + 32 * (q & 1),
-                  *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * q]));
+      for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * q]));
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (c.lane == 0) mbar_arrive_cluster_relaxed(sempty0 + 8 * buf);  // the loads are in registers
+      if (c.lane == 0) mbar_arrive_cluster_relaxed(sempty);  // the loads are in registers
 
       // masked columns take the score -sg * inf, which no max selects and
       // whose exponential is exactly 0
@@ -471,41 +551,43 @@ __device__ __forceinline__ void score_softmax(const Ctx& c) {
             mv[u] = fmin3(mv[u], __uint_as_float(sv[t + 2 * u]), __uint_as_float(sv[t + 2 * u + 1]));
         mr = -fmin3(fminf(mv[0], mv[1]), mv[2], mv[3]);
       }
-      const float mine = (nvr[0] | nvr[1]) ? mr * sg * sl2 : -INFINITY;
-      float other;
-      if (!xchg(c, q4, half, h, xit, mine, &other)) {
-        alive = false;
-        break;
+      const float mx = (nvr[0] | nvr[1]) ? mr * sg * sl2 : -INFINITY;
+      // the maximum after the pass before (another segment's is not used, but
+      // every publication is waited for, so that none is two phases behind)
+      float m_prev = -INFINITY;
+      if (pit > 0) {
+        if (!warp_wait(m_set + other_bar, ((pit - 1) >> 1) & 1u, c.wc)) return;
+        if (!first_pass) m_prev = ld_shared(maxima + other);
       }
-      const float mx = fmaxf(mine, other);
+      const float m_sum = m_ref;  // l is relative to this one
       float alpha = 1.f;
       bool resc = false;
       if (first_pass) {
         m_ref = mx;
-      } else if (mx > m_ref + kRescaleThreshold) {
-        alpha = (m_ref == -INFINITY) ? 0.f : ex2_approx(m_ref - mx);
+      } else if (mx > m_prev + kRescaleThreshold) {
+        alpha = (m_prev == -INFINITY) ? 0.f : ex2_approx(m_prev - mx);
         m_ref = mx;
-        l *= alpha;
         resc = true;
+      } else {
+        m_ref = m_prev;
       }
+      // a last pass's maximum serves nobody: it is published when the sums
+      // have been read
+      if (!last_pass) publish(m_set, maxima, m_ref, c.lane);
+      if (m_sum != m_ref) l *= (m_sum == -INFINITY) ? 0.f : ex2_approx(m_sum - m_ref);
       const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
       const unsigned any = __any_sync(0xffffffffu, resc);
-      const bool last_pass = j0 + kPassBlocks >= g.blk_hi;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int kb = half + 2 * k;
-        if (kb >= nb) continue;
-        const uint32_t ib = it + static_cast<uint32_t>(kb);
+        if (k >= nb) continue;
+        const uint32_t ib = it + static_cast<uint32_t>(k);
         const int r = ib % kNP;
-        if (!warp_wait(bar_addr(c.bars->p_empty[r]), ((ib / kNP) & 1u) ^ 1u, c.wc)) {
-          alive = false;
-          break;
-        }
+        if (!warp_wait(bar_addr(c.bars->p_empty[r]), ((ib / kNP) & 1u) ^ 1u, c.wc)) return;
         const uint32_t full = pfull0 + 8 * r;
         const uint32_t rec = rec0 + r * kRecBytes;
         // one arrival per warp announces its bytes: each lane's P row, for a
         // pass's first block and the segment's last its factors, a flag
-        const bool meta = kb == 0 || (last_pass && kb == nb - 1);
+        const bool meta = k == 0 || (last_pass && k == nb - 1);
         if (c.lane == 0) mbar_arrive_expect_tx_cluster_relaxed(full, 32 * (128 + (meta ? 16 : 0)) + 4);
         float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
@@ -529,73 +611,74 @@ __device__ __forceinline__ void score_softmax(const Ctx& c) {
                         full);
         }
         l += sum0 + sum1;
-        if (c.lane == 0) st_async_b32(rec + kPBytes + kMetaBytes + q4 * 4, (kb == 0 && any) ? 1u : 0u, full);
-        if (kb == 0 && !(last_pass && nb == 1))
-          st_async_v4(rec + kPBytes + h * 16,
-                      make_uint4(__float_as_uint(alpha), __float_as_uint(m_ref), __float_as_uint(l), 0u), full);
-      }
-      if (!alive) break;
-      float ltot = l;
-      if (last_pass) {
-        float lo;
-        if (!xchg(c, q4, half, h, xit, l, &lo)) {
-          alive = false;
-          break;
-        }
-        ltot = l + lo;
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int kb = half + 2 * k;
-        if (!(last_pass && kb == nb - 1)) continue;
-        const uint32_t ib = it + static_cast<uint32_t>(kb);
-        const int r = ib % kNP;
-        st_async_v4(rec0 + r * kRecBytes + kPBytes + h * 16,
-                    make_uint4(__float_as_uint(kb == 0 ? alpha : 1.f), __float_as_uint(m_ref), __float_as_uint(ltot),
-                               0u),
-                    pfull0 + 8 * r);
+        if (c.lane == 0) st_async_b32(rec + kPBytes + kMetaBytes + q4 * 4, (k == 0 && any) ? 1u : 0u, full);
+        if (k == 0 && !(last_pass && nb == 1))
+          st_async_v4(rec + kPBytes + h * 16, make_uint4(__float_as_uint(alpha), __float_as_uint(m_ref), 0u, 0u), full);
       }
       it += static_cast<uint32_t>(nb);
+      if (!last_pass) {
+        if (j0 + 2 * kPassBlocks >= g.blk_hi) publish(l_set, sums, l, c.lane);
+        continue;
+      }
+      float ltot = l;
+      if (!first_pass) {  // the other half's sum, relative to the maximum after its last pass
+        if (!warp_wait(l_set + other_bar, joined & 1u, c.wc)) return;
+        ++joined;
+        const float lo = ld_shared(sums + other);
+        ltot += m_prev == m_ref ? lo : lo * ((m_prev == -INFINITY) ? 0.f : ex2_approx(m_prev - m_ref));
+      }
+      publish(m_set, maxima, m_ref, c.lane);
+      const int r = (it - 1) % kNP;
+      st_async_v4(rec0 + r * kRecBytes + kPBytes + h * 16,
+                  make_uint4(__float_as_uint(nb == 1 ? alpha : 1.f), __float_as_uint(m_ref), __float_as_uint(ltot), 0u),
+                  pfull0 + 8 * r);
     }
   }
 }
 
 // ------------------------------------------------------------------ value pair
 
-__device__ __forceinline__ void value_tma(const Ctx& c, const CUtensorMap* kmap) {
+// One elected thread, as score_feed.
+__device__ __forceinline__ void value_feed(const Ctx& c, const CUtensorMap* kmap4) {
   const ChunkParams& p = *c.p;
   Walker w;
   w.init(p, c.engine);
   Seg g;
-  BlockCursor cur;
-  uint32_t vit = 0;
-  const int col0 = 256 * (c.rank - 2);  // this CTA's half of the latent
-  if (c.lane == 0) prefetch_tmap(kmap);
+  uint32_t slot = 0, parity = 1;
+  const int chunk0 = 4 * (c.rank - 2);  // this CTA's half of the latent
+  prefetch_tmap(kmap4);
+  auto fetch = [&](const Seg& sg, int j) { return p.block_table[size_t(sg.b) * p.max_blocks + j]; };
   bool more = w.next(g);
-  if (more) cur.reset(p, g, c.lane);
+  // ids are read two blocks early
+  int id0 = more ? fetch(g, g.blk_lo) : 0, id1 = more && g.blk_lo + 1 < g.blk_hi ? fetch(g, g.blk_lo + 1) : 0;
   while (more) {
     Seg gn = g;
-    BlockCursor cn = cur;
-    for (int j = g.blk_lo; j < g.blk_hi; ++j, ++vit) {
-      if (j + 1 == g.blk_hi) {
+    int n0 = 0, n1 = 0;
+    for (int j = g.blk_lo; j < g.blk_hi; ++j) {
+      const int id = id0;
+      id0 = id1;
+      if (j + 2 < g.blk_hi) id1 = fetch(g, j + 2);
+      if (j == g.blk_lo) {
         more = w.next(gn);
-        if (more) cn.reset(p, gn, c.lane);
+        if (more) {
+          n0 = fetch(gn, gn.blk_lo);
+          if (gn.blk_lo + 1 < gn.blk_hi) n1 = fetch(gn, gn.blk_lo + 1);
+        }
       }
-      int blk;
-      block_rows(p, g, cur, j, c.lane, &blk);
-      const int s = vit % kVSlots;
-      if (!warp_wait(bar_addr(c.bars->v_empty[s]), ((vit / kVSlots) & 1u) ^ 1u, c.wc)) return;
-      if (c.lane == 0) {
-        const uint32_t full = bar_addr(c.bars->v_full[s]);
-        mbar_arrive_expect_tx(full, kVSlot);
-        const uint32_t dst = c.base + v_slot_off(s);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tma_load_2d(dst + q * kBlkChunk, kmap, col0 + 64 * q, blk * kBlock, full);
+      const int row = id >= 0 && id < p.num_blocks ? id * kBlock : 0;
+      if (!spin_phase(bar_addr(c.bars->v_empty[0]) + 8 * slot, parity, c.wc)) return;
+      const uint32_t full = bar_addr(c.bars->v_full[0]) + 8 * slot;
+      mbar_arrive_expect_tx(full, kVSlot);
+      const uint32_t dst = c.base + v_slot_off(0) + slot * kVSlot;
+      tma_load_chunks(dst, kmap4, row, chunk0, full);
+      if (++slot == kVSlots) {
+        slot = 0;
+        parity ^= 1u;
       }
-      __syncwarp();
     }
     g = gn;
-    cur = cn;
+    id0 = n0;
+    id1 = n1;
   }
 }
 
@@ -916,7 +999,7 @@ __device__ __forceinline__ void value_epilogue(const Ctx& c) {
 // ------------------------------------------------------------------ kernels
 
 __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
-chunk_sm100_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap,
+chunk_sm100_kernel(const __grid_constant__ ChunkMaps maps,
                    const ChunkParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t base = smem_u32(smem_raw);
@@ -929,15 +1012,16 @@ chunk_sm100_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       mbar_init(bar_addr(bars->k_full[s]), 1);
       mbar_init(bar_addr(bars->k_empty[s]), 1);
     }
-    for (int ch = 0; ch < kChunks; ++ch) {
-      mbar_init(bar_addr(bars->q_full[ch]), 1);
-      mbar_init(bar_addr(bars->q_empty[ch]), 1);
-    }
+    mbar_init(bar_addr(bars->q_full), 1);
+    mbar_init(bar_addr(bars->q_empty), 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar_addr(bars->s_full[s]), 1);
-      mbar_init(bar_addr(bars->s_empty[s]), 16);   // eight softmax warps of two CTAs
+      mbar_init(bar_addr(bars->s_empty[s]), 8);    // four softmax warps of two CTAs
+      for (int q = 0; q < 4; ++q) {
+        mbar_init(bar_addr(bars->m_set[s][q]), 1);
+        mbar_init(bar_addr(bars->l_set[s][q]), 1);
+      }
     }
-    for (int q = 0; q < 4; ++q) mbar_init(bar_addr(bars->xchg[q]), 64);  // two warps
     for (int r = 0; r < kNP; ++r) {
       mbar_init(bar_addr(bars->p_empty[r]), 1);    // PV commit, or the epilogue (segment end)
       mbar_init(bar_addr(bars->p_full[r]), 4);     // the four softmax warps of one half
@@ -984,13 +1068,19 @@ chunk_sm100_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     // issued, the call reads as one that gave up
     if (threadIdx.x == 0) atomicOr(p.err, kErrTimeout);
   } else if (rank < 2) {
-    if (warp == 0) score_tma_k(c, &kmap);
-    else if (warp == 1 && rank == 0) score_mma(c);
-    else if (warp == 2) score_tma_q(c, &qmap);
+    if (warp == 0) {
+      if (elect_one()) score_feed(c, &maps.k, &maps.k2, &maps.q);
+      __syncwarp();
+    }
+    if (warp == 1 && rank == 0) score_mma(c);
+    else if (warp == 2) score_tma_q(c, &maps.q);
     else if (warp >= 4) score_softmax(c);
   } else {
-    if (warp == 0) value_tma(c, &kmap);
-    else if (warp == 1 && rank == 2) value_mma(c);
+    if (warp == 0) {
+      if (elect_one()) value_feed(c, &maps.k4);
+      __syncwarp();
+    }
+    if (warp == 1 && rank == 2) value_mma(c);
     else if (warp == 2) value_fixup(c);
     else if (warp == 3) value_relay(c);
     else if (warp >= 4) value_epilogue(c);
@@ -1215,8 +1305,7 @@ int chunk_sm100_max_clusters() {
   return n;
 }
 
-cudaError_t launch_chunk_sm100(const ChunkParams& p, const CUtensorMap& kmap, const CUtensorMap& qmap,
-                               cudaStream_t stream) {
+cudaError_t launch_chunk_sm100(const ChunkParams& p, const ChunkMaps& maps, cudaStream_t stream) {
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -1237,7 +1326,7 @@ cudaError_t launch_chunk_sm100(const ChunkParams& p, const CUtensorMap& kmap, co
   cfg.gridDim = dim3(4 * p.P);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
-  if (cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_sm100_kernel, kmap, qmap, p); e != cudaSuccess) return e;
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_sm100_kernel, maps, p); e != cudaSuccess) return e;
   cfg.gridDim = dim3(p.P, kMergeGrid);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.dynamicSmemBytes = 0;

@@ -139,8 +139,11 @@ struct ChunkParams {
 };
 // Plan, attention and merge kernels.  kmap as for launch_weigh; qmap: q as
 // [T*H, 576] with 64 x 128 boxes.
-cudaError_t launch_chunk_sm100(const ChunkParams& p, const CUtensorMap& kmap, const CUtensorMap& qmap,
-                               cudaStream_t stream);
+struct ChunkMaps {
+  CUtensorMap q;          // query rows, boxes of 128 rows x 64 columns
+  CUtensorMap k, k2, k4;  // the cache: one, two and four 64-column chunks of 64 rows
+};
+cudaError_t launch_chunk_sm100(const ChunkParams& p, const ChunkMaps& maps, cudaStream_t stream);
 int chunk_sm100_max_clusters();
 
 struct WeighParams {

@@ -43,8 +43,24 @@ __device__ __forceinline__ void pair_mma_ss(uint32_t d, uint64_t a, uint64_t b, 
       : "memory");
 }
 
+// The same with A in TMEM: row i of a CTA's half of M in lane i, two
+// consecutive elements of K per 32-bit column, from column `a` on.
+__device__ __forceinline__ void pair_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// In both CTAs, 128 rows x 32 bytes from shared memory into eight columns of
+// TMEM.  MMAs that this thread issues later read the copied values.
+__device__ __forceinline__ void pair_cp_128x32b(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.128x256b [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
 // Arrive on the barrier at local offset `bar` in every CTA of `mask` once all
-// MMAs this thread issued have completed.
+// MMAs and copies this thread issued have completed.
 __device__ __forceinline__ void pair_commit(uint32_t bar, uint16_t mask) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
@@ -59,6 +75,23 @@ __device__ __forceinline__ void pair_tma_load_2d(uint32_t dst, const CUtensorMap
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
       " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+// The same for a box of a 3-D map [chunk][row][64 columns], one instruction for
+// several 64-column chunks.
+__device__ __forceinline__ void pair_tma_load_3d(uint32_t dst, const CUtensorMap* map, int row, int chunk, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(chunk), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_chunks(uint32_t dst, const CUtensorMap* map, int row, int chunk, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(chunk), "r"(bar)
       : "memory");
 }
 

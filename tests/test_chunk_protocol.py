@@ -9,9 +9,20 @@ import random
 
 import pytest
 
-from tests.test_pipeline_protocol import Bar, _passes, _patterns
+from tests.test_pipeline_protocol import Bar, _patterns
 
-K_SLOTS, V_SLOTS, N_REC, CHUNKS = 5, 4, 4, 9
+K_SLOTS, V_SLOTS, N_REC, CHUNKS, PASS = 13, 4, 4, 9, 2
+Q_SLOTS = CHUNKS - 1                                 # chunks of Q that go through the ring to TMEM
+
+
+def _passes(lo, hi):
+    for j in range(lo, hi, PASS):
+        yield j, min(PASS, hi - j)
+
+
+def _k_slots(lo, hi):
+    """Slots of a segment's K: two chunks each, over the ends of passes."""
+    return (CHUNKS * len(list(_passes(lo, hi))) + 1) // 2
 
 
 def roles(segs, flags, counts):
@@ -27,16 +38,16 @@ def roles(segs, flags, counts):
         bar(f"k_full{s}", 2)                         # rank 0's arrival with its bytes, rank 1's bytes
         for r in (0, 1):
             bar(at(f"k_empty{s}", r), 1)
-    for ch in range(CHUNKS):
-        bar(f"q_full{ch}", 2)
-        for r in (0, 1):
-            bar(at(f"q_empty{ch}", r), 1)
+    bar("q_full", 2)                                 # the last chunk of Q
+    for r in (0, 1):
+        bar(at("q_empty", r), 1)
     for s in range(2):
-        bar(f"s_empty{s}", 16)
+        bar(f"s_empty{s}", 8)
         for r in (0, 1):
             bar(at(f"s_full{s}", r), 1)
-    for r in (0, 1):
-        bar(at("xchg", r), 2)
+        for r in (0, 1):                             # one quadrant's warp of each half
+            bar(at(f"m_set{s}", r), 1)
+            bar(at(f"l_set{s}", r), 1)
     for i in range(N_REC):
         for r in (0, 1):
             bar(at(f"p_empty{i}", r), 1)
@@ -54,70 +65,90 @@ def roles(segs, flags, counts):
     bar("corr_done", 16)
     bar("o_free", 16)
 
-    def score_k(rank):
+    def score_tma(rank):
         fit = 0
         for lo, hi in segs:
-            for _ in _passes(lo, hi):
-                for _ch in range(CHUNKS):
-                    s = fit % K_SLOTS
-                    yield at(f"k_empty{s}", rank), ((fit // K_SLOTS) & 1) ^ 1, fit // K_SLOTS - 1
-                    B[f"k_full{s}"].arrive()
-                    fit += 1
+            for _ in range(Q_SLOTS + _k_slots(lo, hi)):
+                s = fit % K_SLOTS
+                yield at(f"k_empty{s}", rank), ((fit // K_SLOTS) & 1) ^ 1, fit // K_SLOTS - 1
+                B[f"k_full{s}"].arrive()
+                fit += 1
 
     def score_q(rank):
         for seg, _ in enumerate(segs):
-            for ch in range(CHUNKS):
-                yield at(f"q_empty{ch}", rank), (seg & 1) ^ 1, seg - 1
-                B[f"q_full{ch}"].arrive()
+            yield at("q_empty", rank), (seg & 1) ^ 1, seg - 1
+            B["q_full"].arrive()
 
     def score_mma():
         fit = pit = 0
+
+        def full():
+            return f"k_full{fit % K_SLOTS}", (fit // K_SLOTS) & 1, fit // K_SLOTS
+
+        def done(name):
+            for r in (0, 1):
+                B[at(name, r)].arrive()
+
         for seg, (lo, hi) in enumerate(segs):
+            if pit > 0:                              # the MMAs that read the last segment's Q
+                yield at(f"s_full{(pit - 1) & 1}", 0), ((pit - 1) >> 1) & 1, (pit - 1) >> 1
+            for _ in range(Q_SLOTS):
+                yield full()
+                done(f"k_empty{fit % K_SLOTS}")
+                fit += 1
+            half = 0
             for j, nb in _passes(lo, hi):
+                last = j + nb >= hi
                 yield f"s_empty{pit & 1}", ((pit >> 1) & 1) ^ 1, (pit >> 1) - 1
                 for ch in range(CHUNKS):
-                    s = fit % K_SLOTS
-                    if j == lo:
-                        yield f"q_full{ch}", seg & 1, seg
-                    yield f"k_full{s}", (fit // K_SLOTS) & 1, fit // K_SLOTS
-                    for r in (0, 1):
-                        B[at(f"k_empty{s}", r)].arrive()
-                        if j + nb >= hi:
-                            B[at(f"q_empty{ch}", r)].arrive()
-                    fit += 1
-                for r in (0, 1):
-                    B[at(f"s_full{pit & 1}", r)].arrive()
+                    if half == 0:
+                        yield full()
+                    if ch == CHUNKS - 1:
+                        if j == lo:
+                            yield "q_full", seg & 1, seg
+                        if last:
+                            done("q_empty")
+                    if half or (last and ch == CHUNKS - 1):
+                        done(f"k_empty{fit % K_SLOTS}")
+                        fit += 1
+                        half = 0
+                    else:
+                        half = 1
+                done(f"s_full{pit & 1}")
                 pit += 1
 
     def softmax(rank, half):
-        it = pit = xit = 0
+        it = pit = joined = 0
         for lo, hi in segs:
             for j0, nb in _passes(lo, hi):
-                yield at(f"s_full{pit & 1}", rank), (pit >> 1) & 1, pit >> 1
-                B[f"s_empty{pit & 1}"].arrive(4)
-                pit += 1
-                B[at("xchg", rank)].arrive()
-                yield at("xchg", rank), xit & 1, xit
-                xit += 1
-                last = j0 + nb >= hi
-                final = None
-                for kb in (half, half + 2):
-                    if kb >= nb:
-                        continue
+                if pit & 1 != half:
+                    it += nb
+                    pit += 1
+                    continue
+                first, last = j0 == lo, j0 + nb >= hi
+                yield at(f"s_full{half}", rank), (pit >> 1) & 1, pit >> 1
+                B[f"s_empty{half}"].arrive(4)
+                if pit > 0:
+                    yield at(f"m_set{half ^ 1}", rank), ((pit - 1) >> 1) & 1, (pit - 1) >> 1
+                if not last:
+                    B[at(f"m_set{half}", rank)].arrive()
+                for kb in range(nb):
                     ib = it + kb
                     r = ib % N_REC
                     yield at(f"p_empty{r}", rank), ((ib // N_REC) & 1) ^ 1, ib // N_REC - 1
-                    if last and kb == nb - 1:
-                        final = r
-                    else:
+                    if not (last and kb == nb - 1):
                         B[at(f"p_full{r}", rank + 2)].arrive(4)
-                if last:
-                    B[at("xchg", rank)].arrive()
-                    yield at("xchg", rank), xit & 1, xit
-                    xit += 1
-                if final is not None:
-                    B[at(f"p_full{final}", rank + 2)].arrive(4)
                 it += nb
+                if not last:
+                    if j0 + 2 * PASS >= hi:
+                        B[at(f"l_set{half}", rank)].arrive()
+                else:
+                    if not first:
+                        yield at(f"l_set{half ^ 1}", rank), joined & 1, joined
+                        joined += 1
+                    B[at(f"m_set{half}", rank)].arrive()
+                    B[at(f"p_full{(it - 1) % N_REC}", rank + 2)].arrive(4)
+                pit += 1
 
     def blocks():
         i = 0
@@ -185,7 +216,7 @@ def roles(segs, flags, counts):
 
     procs = {"score_mma": score_mma(), "value_mma": value_mma()}
     for r in (0, 1):
-        procs |= {f"k{r}": score_k(r), f"q{r}": score_q(r), f"soft{r}a": softmax(r, 0), f"soft{r}b": softmax(r, 1),
+        procs |= {f"k{r}": score_tma(r), f"q{r}": score_q(r), f"soft{r}a": softmax(r, 0), f"soft{r}b": softmax(r, 1),
                   f"v{r + 2}": value_tma(r + 2), f"relay{r + 2}": relay(r + 2), f"fix{r + 2}": fixup(r + 2), f"epi{r + 2}": epilogue(r + 2)}
     return B, procs
 
@@ -220,6 +251,6 @@ def test_protocol_finishes_in_every_interleaving():
             assert res is True, f"segments {segs}, seed {seed}: blocked {res}"
 
 
-@pytest.mark.parametrize("name,count", [("p_empty", 2), ("v_ready", 3), ("q_full", 3), ("s_empty", 17), ("corr_done", 17)])
+@pytest.mark.parametrize("name,count", [("p_empty", 2), ("v_ready", 3), ("q_full", 3), ("s_empty", 9), ("m_set", 2), ("corr_done", 17)])
 def test_model_finds_planted_counts(name, count):
     assert all(simulate([(0, 40), (0, 9), (0, 30)], seed, {name: count}) is not True for seed in range(3))
