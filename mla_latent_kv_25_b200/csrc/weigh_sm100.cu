@@ -173,6 +173,8 @@ __device__ __forceinline__ bool produce(const Ctx& c, const CUtensorMap* qmap, c
   Bars* bars = c.bars;
   const uint32_t res_bar = map_to_rank(bar_addr(bars->res_full), c.lead);
   const uint32_t full0 = map_to_rank(bar_addr(bars->ring_full[0]), c.lead);
+  const uint32_t own_full0 = bar_addr(bars->ring_full[0]), empty0 = bar_addr(bars->ring_empty[0]);
+  const CUtensorMap* stream = q.stay ? kmap : qmap;
   const bool switched = ring.mode(q.stay);
   const uint32_t ring0 = c.base + ring_off(q.stay);
   const int active = active_pairs(c, q);
@@ -207,13 +209,15 @@ __device__ __forceinline__ bool produce(const Ctx& c, const CUtensorMap* qmap, c
     }
     for (int i = c.pair; i < q.tiles; i += active) {
       const int row = q.row0 + kStreamRows * i + c.rank * (tile_rows(q, i) / 2);
-      for (int ch = 0; ch < kChunks; ++ch) {
-        if (!wait_phase(bar_addr(bars->ring_empty[ring.slot]), ring.phase() ^ 1u, c.wc)) return false;
-        const uint32_t full = full0 + 8 * ring.slot;
+      const int r0 = q.stay ? y0 : row, r1 = q.stay ? y1 : row + 64;
+#pragma unroll 1
+      for (int x = 0; x < 64 * kChunks; x += 64) {
+        const uint32_t at = 8 * ring.slot;
+        if (!wait_phase(empty0 + at, ring.phase() ^ 1u, c.wc)) return false;
+        if (c.rank == 0) mbar_arrive_expect_tx(own_full0 + at, 2 * kChunk);
         const uint32_t dst = ring0 + ring.slot * kChunk;
-        if (c.rank == 0) mbar_arrive_expect_tx(bar_addr(bars->ring_full[ring.slot]), 2 * kChunk);
-        pair_tma_load_2d(dst, q.stay ? kmap : qmap, 64 * ch, q.stay ? y0 : row, full);
-        pair_tma_load_2d(dst + kHalf, q.stay ? kmap : qmap, 64 * ch, q.stay ? y1 : row + 64, full);
+        pair_tma_load_2d(dst, stream, x, r0, full0 + at);
+        pair_tma_load_2d(dst + kHalf, stream, x, r1, full0 + at);
         ring.next();
       }
       if (queries_due) {
@@ -456,10 +460,12 @@ weigh_sm100_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     if (c.pair >= active_pairs(c, q)) continue;
     int ok = 1;
     if (warp == 0) {
-      if (q.tiles > 0 && lane == 0) ok = produce(c, &qmap, &kmap, g, q, rit, ring) ? 1 : 0;
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-    } else if (warp == 1) {
       // counters live in the elected thread, the same one every time
+      if (q.tiles > 0 && elect_one()) {
+        if (!produce(c, &qmap, &kmap, g, q, rit, ring)) ok = 0;
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    } else if (warp == 1) {
       if (q.tiles > 0 && c.rank == 0 && elect_one()) {
         if (!multiply(c, (g.blk_hi - g.blk_lo + kTileBlocks - 1) / kTileBlocks, q, rit, ring, ait)) ok = 0;
       }
