@@ -670,7 +670,7 @@ mla_status_t mla_chunk_attend(const void* q, const int32_t* q_offsets, int T, ml
   p.tile_off = reinterpret_cast<int*>(wsb + lay.tile_off);
   p.tiles = reinterpret_cast<int4*>(wsb + lay.tiles);
   p.pre = reinterpret_cast<long long*>(wsb + lay.pre);
-  static_assert(sizeof(ChunkEngine) == 24, "chunk_layout's engine records");
+  static_assert(sizeof(ChunkEngine) == 64, "chunk_layout's engine records");
   p.engines = reinterpret_cast<ChunkEngine*>(wsb + lay.engines);
   p.lse_part = reinterpret_cast<float*>(wsb + lay.lse_part);
   p.o_part = reinterpret_cast<float*>(wsb + lay.o_part);

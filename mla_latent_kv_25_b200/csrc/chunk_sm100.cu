@@ -169,8 +169,9 @@ __device__ __forceinline__ int tile_of(const long long* pre, int nt, long long x
 // us instead of 4.9 us for a tile's output).
 struct Walker {
   const ChunkParams* p;
-  long long s, e;
-  int t, nt, engine, count;
+  long long s, e, a0, z0;  // range; units of tile t0
+  int4 tile0;
+  int t, nt, t0, engine, count;
 
   __device__ __forceinline__ void init(const ChunkParams& pp, int engine_) {
     p = &pp;
@@ -179,14 +180,19 @@ struct Walker {
     const ChunkEngine r = pp.engines[engine_];
     s = r.s;
     e = r.e;
-    t = r.t;
+    a0 = r.a;
+    z0 = r.z;
+    tile0 = r.tile;
+    t = t0 = r.t;
     nt = r.nt;
   }
 
   __device__ __forceinline__ bool next(Seg& g) {
     for (; t < nt; ++t) {
-      const long long a = p->pre[t] + kTileUnits, z = p->pre[t + 1];
-      const int4 info = p->tiles[t];
+      // the first tile came with the range: one load later saved
+      const bool known = t == t0;
+      const long long a = (known ? a0 : p->pre[t]) + kTileUnits, z = known ? z0 : p->pre[t + 1];
+      const int4 info = known ? tile0 : p->tiles[t];
       if (a - kTileUnits >= e) return false;
       const long long lo = s > a ? s : a, hi = e < z ? e : z;
       if (lo >= hi) continue;  // no cached token, or none of its blocks in the range
@@ -755,7 +761,7 @@ __device__ __forceinline__ void value_relay(const Ctx& c) {
     if (c.lane == 0) {
       for (int j = g.blk_lo; j < g.blk_hi; ++j, ++it) {
         const int r = it % kNP;
-        if (!wait_phase(bar_addr(c.bars->p_full[r]), (it / kNP) & 1u, c.wc)) {
+        if (!spin_phase(bar_addr(c.bars->p_full[r]), (it / kNP) & 1u, c.wc)) {
           ok = 0;
           break;
         }
@@ -788,14 +794,14 @@ __device__ __forceinline__ bool value_mma_segment(const Ctx& c, const Seg& g, ui
   const uint64_t p0 = plain_desc(c.base + rec_off(0), kPCoreK, 128);
   const uint64_t v0 = sw128_desc(c.base + v_slot_off(0), kBlkChunk, 1024);
   if (seg > 0) {
-    if (!wait_phase(bar_addr(bars->o_free), (seg - 1) & 1u, c.wc)) return false;
+    if (!spin_phase(bar_addr(bars->o_free), (seg - 1) & 1u, c.wc)) return false;
     tc_fence_after();
   }
   bool p_ok = false, v_ok = false;
   for (int j = g.blk_lo; j < g.blk_hi; ++j, ++it) {
     const uint32_t r = it % kNP, s = it % kVSlots;
     const bool first = (j == g.blk_lo), last = (j == g.blk_hi - 1);
-    if (!p_ok && !wait_phase(bar_addr(bars->p_ready[r]), (it / kNP) & 1u, c.wc)) return false;
+    if (!p_ok && !spin_phase(bar_addr(bars->p_ready[r]), (it / kNP) & 1u, c.wc)) return false;
     const uint32_t flags = *reinterpret_cast<volatile uint32_t*>(&bars->flag[r][0]) |
                            *reinterpret_cast<volatile uint32_t*>(&bars->flag[r][1]);
     if (flags && !first) {
@@ -804,7 +810,7 @@ __device__ __forceinline__ bool value_mma_segment(const Ctx& c, const Seg& g, ui
       ++ncorr;
       tc_fence_after();
     }
-    if (!v_ok && !wait_phase(bar_addr(bars->v_ready[s]), (it / kVSlots) & 1u, c.wc)) return false;
+    if (!v_ok && !spin_phase(bar_addr(bars->v_ready[s]), (it / kVSlots) & 1u, c.wc)) return false;
     const uint32_t nx = it + 1;
     p_ok = mbar_test_wait(bar_addr(bars->p_ready[nx % kNP]), (nx / kNP) & 1u);
     v_ok = mbar_test_wait(bar_addr(bars->v_ready[nx % kVSlots]), (nx / kVSlots) & 1u);
@@ -933,34 +939,39 @@ __device__ __forceinline__ void value_epilogue(const Ctx& c) {
       uint8_t* stage = c.gbase + stage_off(c.warp - 4);
       const int row0 = 128 * (c.rank - 2) + q4 * 32;  // the warp's first row
       if (g.slot < 0) {
-        // all of the row's half as bf16 in registers, so that the next tile's
-        // MMAs may start on O before the rows are stored
-        uint4 o[8][4];
-#pragma unroll
-        for (int ch = 0; ch < 8; ++ch) {
-          uint32_t v[32];
-          tmem_ld32(c.tmem + lane_off + ocol + 32 * ch, v);
+        if (!release_record()) return;
+        // A loop: unrolled, with all of the row's half in registers before the
+        // first store, O is free earlier, but fetching its instructions costs
+        // more (a tile's output 4.1 us against 3.2; calls of many tiles 3 % faster,
+        // small ones 8 % slower).
+#pragma unroll 1
+        for (int ch = 0; ch < 8; ch += 2) {
+          uint4 o[2][4];
+          uint32_t v[2][32];
+          tmem_ld32(c.tmem + lane_off + ocol + 32 * ch, v[0]);
+          tmem_ld32(c.tmem + lane_off + ocol + 32 * ch + 32, v[1]);
           tmem_ld_wait();
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t w4[4];
+          for (int k = 0; k < 2; ++k) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[8 * q + 2 * e]) * inv,
-                                                        __uint_as_float(v[8 * q + 2 * e + 1]) * inv);
-              w4[e] = *reinterpret_cast<uint32_t*>(&b2);
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w4[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[k][8 * q + 2 * e]) * inv,
+                                                          __uint_as_float(v[k][8 * q + 2 * e + 1]) * inv);
+                w4[e] = *reinterpret_cast<uint32_t*>(&b2);
+              }
+              o[k][q] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
             }
-            o[ch][q] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
           }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (c.lane == 0) mbar_arrive_cluster_relaxed(o_free);
-        if (!release_record()) return;
-#pragma unroll
-        for (int ch = 0; ch < 8; ch += 2) {
+          if (ch == 6) {
+            tc_fence_before();
+            __syncwarp();
+            if (c.lane == 0) mbar_arrive_cluster_relaxed(o_free);
+          }
           const int col = latent_of(ocol + 32 * ch);
-          store_rows(stage, c.lane, o[ch], o[ch + 1], [&](int r) -> uint8_t* {
+          store_rows(stage, c.lane, o[0], o[1], [&](int r) -> uint8_t* {
             if (row0 + r >= g.rows) return nullptr;
             return reinterpret_cast<uint8_t*>(p.out + (size_t(g.row0) + row0 + r) * kDc + col);
           });
@@ -1132,11 +1143,20 @@ __device__ T block_scan(T v, T* warp_sums, T* total) {
 }
 
 // The tile list: tiles of up to 256 / H tokens of one sequence, and the
-// running count of the cache blocks they read.
-__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p) {
+// running count of the cache blocks they read.  kFew: at most kPlanFew
+// sequences and tiles, whose lists stay in shared memory between the steps
+// (1.4 us instead of 2.1, at the head of every small call).
+template <bool kFew>
+__global__ void __launch_bounds__(kFew ? kPlanFew : kPlanThreads) chunk_plan_kernel(const ChunkParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ long long sums[32];
   __shared__ int isums[32];
+  __shared__ int few_off[kFew ? kPlanFew + 1 : 1], few_a[kFew ? kPlanFew : 1], few_n[kFew ? kPlanFew : 1],
+      few_len[kFew ? kPlanFew : 1];
+  __shared__ long long few_pre[kFew ? kPlanFew + 1 : 1];
+  __shared__ int4 few_tile[kFew ? kPlanFew : 1];
+  int* const off = kFew ? few_off : p.tile_off;
+  const long long* const pre = kFew ? few_pre : p.pre;
   const int per = kTileRows / p.H;
   int nt = 0;
   for (int b0 = 0; b0 < p.B; b0 += blockDim.x) {
@@ -1144,26 +1164,32 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
     int tiles = 0;
     if (b < p.B) {
       const int a = p.q_offsets[b], e = p.q_offsets[b + 1];
-      checked_len(p.seq_lens, b, p.max_blocks, p.err);
+      const int len = checked_len(p.seq_lens, b, p.max_blocks, p.err);
       if (a < 0 || e < a || e > p.T)
         atomicOr(p.err, kErrSeqTooLong);
       else
         tiles = (e - a + per - 1) / per;
+      if (kFew) {
+        few_a[b] = a;
+        few_n[b] = e - a;
+        few_len[b] = len;
+      }
     }
     int total;
     const int incl = block_scan(tiles, isums, &total);
     // only offsets that decrease somewhere can ask for more tiles than T
     // tokens fill: what is over is left out
     if (b < p.B) {
-      p.tile_off[b] = min(p.max_tiles, nt + incl - tiles);
+      off[b] = min(p.max_tiles, nt + incl - tiles);
       if (nt + incl > p.max_tiles) atomicOr(p.err, kErrSeqTooLong);
     }
     nt = min(p.max_tiles, nt + total);
   }
   if (threadIdx.x == 0) {
-    p.tile_off[p.B] = nt;
+    off[p.B] = nt;
     *p.n_tiles = nt;
     p.pre[0] = 0;
+    if (kFew) few_pre[0] = 0;
   }
   __syncthreads();
   long long blocks = 0;
@@ -1171,33 +1197,44 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
     const int t = t0 + threadIdx.x;
     long long mine = 0;
     if (t < nt) {
-      int lo = 0, hi = p.B;  // tile_off[lo] <= t < tile_off[hi]
+      int lo = 0, hi = p.B;  // off[lo] <= t < off[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (p.tile_off[mid] <= t) lo = mid; else hi = mid;
+        if (off[mid] <= t) lo = mid; else hi = mid;
       }
-      const int a = p.q_offsets[lo], n = p.q_offsets[lo + 1] - a;
-      const int j = (t - p.tile_off[lo]) * per;
+      const int a = kFew ? few_a[lo] : p.q_offsets[lo], n = kFew ? few_n[lo] : p.q_offsets[lo + 1] - a;
+      const int seen = kFew ? few_len[lo] : checked_len(p.seq_lens, lo, p.max_blocks, nullptr);
+      const int j = (t - off[lo]) * per;
       const int tok = min(per, n - j);
       // the tile's last token sees the sequence without the n - j - tok tokens behind it
-      const int len = max(0, checked_len(p.seq_lens, lo, p.max_blocks, nullptr) - (n - j - tok));
-      p.tiles[t] = make_int4((a + j) * p.H, tok * p.H, lo, len);
+      const int len = max(0, seen - (n - j - tok));
+      const int4 tile = make_int4((a + j) * p.H, tok * p.H, lo, len);
+      p.tiles[t] = tile;
+      if (kFew) few_tile[t] = tile;
       mine = len > 0 ? nblocks_of(len) + kTileUnits : 0;
     }
     long long total;
     const long long incl = block_scan(mine, sums, &total);
-    if (t < nt) p.pre[t + 1] = blocks + incl;
+    if (t < nt) {
+      p.pre[t + 1] = blocks + incl;
+      if (kFew) few_pre[t + 1] = blocks + incl;
+    }
     blocks += total;
   }
   // every engine's range and first tile (t = nt: none)
   __syncthreads();
   const int P = engines_of(p, blocks);
   for (int e = threadIdx.x; e < p.P; e += blockDim.x) {
-    ChunkEngine r = {0, 0, nt, nt};
+    ChunkEngine r = {};
+    r.t = r.nt = nt;
+    r.total = blocks;
     if (e < P) {
       r.s = range_start(e, blocks, P);
       r.e = range_start(e + 1, blocks, P);
-      r.t = tile_of(p.pre, nt, r.s);
+      r.t = tile_of(pre, nt, r.s);
+      r.a = pre[r.t];
+      r.z = pre[r.t + 1];
+      r.tile = kFew ? few_tile[r.t] : p.tiles[r.t];
     }
     p.engines[e] = r;
   }
@@ -1230,7 +1267,10 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkP
       for (int r = wid; r < p.tiles[t].y; r += kMergeGrid * kMergeWarps) fill_row(p, size_t(p.tiles[t].x) + r, NAN, lane);
     return;
   }
-  const long long total = p.pre[nt];
+  const int e1 = blockIdx.x + 1;  // the boundary between engines e1 - 1 and e1
+  ChunkEngine r = {};
+  if (e1 < p.P) r = p.engines[e1];
+  const long long s0 = p.engines[blockIdx.x].s;
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     const int a = p.q_offsets[b], e = p.q_offsets[b + 1];
     if (a < 0 || e < a || e > p.T) continue;
@@ -1238,15 +1278,12 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkP
     for (long long r = wid; r < static_cast<long long>(blind) * p.H; r += kMergeGrid * kMergeWarps)
       fill_row(p, size_t(a) * p.H + r, -INFINITY, lane);
   }
+  const long long total = r.total, x = r.s, a = r.a, z = r.z;
   const int P = engines_of(p, total);
-  const int e1 = blockIdx.x + 1;  // the boundary between engines e1 - 1 and e1
   if (e1 >= P) return;
-  const long long x = range_start(e1, total, P), s0 = range_start(e1 - 1, total, P);
-  const int t = p.engines[e1].t;
-  const long long a = p.pre[t], z = p.pre[t + 1];
   // merged at the boundary whose left engine holds the tile's first block
   if (x <= a + kTileUnits || s0 > a + kTileUnits) return;
-  const int4 info = p.tiles[t];
+  const int4 info = r.tile;
   const int row = (wid & 7) * 32 + lane, col4 = (wid >> 3) * (kMergeCols / 4);
   if (row >= info.y) return;
   const int last = engine_of(z - 1, total, P);
@@ -1313,8 +1350,10 @@ cudaError_t launch_chunk_sm100(const ChunkParams& p, const ChunkMaps& maps, cuda
     if (cudaError_t e = set_attributes(); e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  const int threads = p.B <= kPlanFew && p.max_tiles <= kPlanFew ? kPlanFew : kPlanThreads;
-  chunk_plan_kernel<<<1, threads, 0, stream>>>(p);
+  if (p.B <= kPlanFew && p.max_tiles <= kPlanFew)
+    chunk_plan_kernel<true><<<1, kPlanFew, 0, stream>>>(p);
+  else
+    chunk_plan_kernel<false><<<1, kPlanThreads, 0, stream>>>(p);
   if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];

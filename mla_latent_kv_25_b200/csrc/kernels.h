@@ -108,9 +108,12 @@ cudaError_t launch_cache_append_rope(const AppendRopeParams& p, cudaStream_t str
 
 // An engine's share of a chunk call: units [s, e) of the axis that is cut, the
 // first tile in it, and the number of tiles.
-struct __align__(8) ChunkEngine {
-  long long s, e;
-  int t, nt;
+struct __align__(16) ChunkEngine {
+  int4 tile;             // the first tile's entry of the list
+  long long a, z;        // and its units
+  long long s, e;        // range
+  long long total;       // units of all tiles
+  int t, nt;             // first tile, number of tiles
 };
 
 // Ragged chunks of query tokens over the paged cache (mla_chunk_attend).

@@ -84,7 +84,7 @@ inline ChunkLayout chunk_layout(int T, int B, int H, int P) {
   w.tiles = align256(w.tile_off + (size_t(B) + 1) * 4);
   w.pre = align256(w.tiles + size_t(w.max_tiles) * 16);
   w.engines = align256(w.pre + (size_t(w.max_tiles) + 1) * 8);
-  w.lse_part = align256(w.engines + size_t(P) * 24);
+  w.lse_part = align256(w.engines + size_t(P) * 64);
   w.o_part = align256(w.lse_part + size_t(2 * P) * kChunkTileRows * 4);
   w.total = align256(w.o_part + size_t(2 * P) * kChunkTileRows * kDc * 4);
   return w;

@@ -25,11 +25,20 @@ def _k_slots(lo, hi):
     return (CHUNKS * len(list(_passes(lo, hi))) + 1) // 2
 
 
+class Exact(Bar):
+    """Also fails on a wait that passes before its phase is complete (a waiter two phases early)."""
+
+    def passes(self, parity, phase):
+        ok = super().passes(parity, phase)
+        assert not ok or self.done > phase, f"{self.name}: waiter for phase {phase} early ({self.done} done)"
+        return ok
+
+
 def roles(segs, flags, counts):
     B = {}
 
     def bar(name, count):
-        B[name] = Bar(name, counts.get(name.rstrip("0123456789_"), count))
+        B[name] = Exact(name, counts.get(name.rstrip("0123456789_"), count))
 
     def at(name, rank):
         return f"{name}_{rank}"
