@@ -387,9 +387,21 @@ def mla_get_device_error(workspace, stream=None) -> int:
 # time of checking them one property at a time, which a small call would feel)
 # and look for the reason only when it fails.
 
+# The calls below are made once a step or a layer: names bound here, one raw
+# stream handle per call (a check takes 0.36 us instead of 0.55).
+_Tensor, _bf16, _i32, _f32, _f64, _u8 = torch.Tensor, torch.bfloat16, torch.int32, torch.float32, torch.float64, torch.uint8
+
+
+def _handle(stream, dev):
+    """Raw handle of the stream, or of the current one of device `dev`."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
 def _want(t, name, dtype, shape, dev):
     """A contiguous tensor of this dtype and shape on the current device."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.get_device() == dev and t.is_contiguous()
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
             and (shape is None or t.shape == shape)):
         _need(t, name, dtype, shape)
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
@@ -397,7 +409,7 @@ def _want(t, name, dtype, shape, dev):
 
 def _want_rows(t, name, dim, width, dev):
     """bf16 rows with a contiguous last axis on the current device; other strides are free."""
-    if isinstance(t, torch.Tensor) and t.dtype == torch.bfloat16 and t.get_device() == dev and t.dim() == dim:
+    if isinstance(t, _Tensor) and t.dtype is _bf16 and t.get_device() == dev and t.dim() == dim:
         if t.shape[-1] == width and (t.stride(-1) == 1 or width == 1 or t.numel() == 0):
             return
     if not isinstance(t, torch.Tensor):
@@ -446,12 +458,12 @@ def mla_rope(x, pos, freqs, y, *, mscale=1.0, layout="interleaved", inverse=Fals
     _want_rows(y, "y", 3, rot, dev)
     if y.shape != x.shape:
         raise ValueError(f"y: expected shape {tuple(x.shape)}, got {tuple(y.shape)}")
-    _want(pos, "pos", torch.int32, (T,), dev)
-    _want(freqs, "freqs", torch.float64, (rot // 2,), dev)
+    _want(pos, "pos", _i32, (T,), dev)
+    _want(freqs, "freqs", _f64, (rot // 2,), dev)
     xt, xh, _ = x.stride()
     yt, yh, _ = y.stride()
     _check("mla_rope", load().mla_rope(x.data_ptr(), xt, xh, pos.data_ptr(), freqs.data_ptr(), float(mscale),
-                                       _rope_flags(layout, inverse), y.data_ptr(), yt, yh, T, H, rot, _stream(stream)))
+                                       _rope_flags(layout, inverse), y.data_ptr(), yt, yh, T, H, rot, _handle(stream, dev)))
     return y
 
 
@@ -465,33 +477,33 @@ def mla_cache_append_rope(c_kv, k_r, seq_idx, slot, pos, freqs, block_table, cac
     T = c_kv.shape[0]
     if k_r.shape[0] != T:
         raise ValueError(f"k_r: expected {T} rows, got {k_r.shape[0]}")
-    _want(seq_idx, "seq_idx", torch.int32, (T,), dev)
-    _want(slot, "slot", torch.int32, (T,), dev)
-    _want(pos, "pos", torch.int32, (T,), dev)
-    _want(freqs, "freqs", torch.float64, (32,), dev)
+    _want(seq_idx, "seq_idx", _i32, (T,), dev)
+    _want(slot, "slot", _i32, (T,), dev)
+    _want(pos, "pos", _i32, (T,), dev)
+    _want(freqs, "freqs", _f64, (32,), dev)
     B, mb, NB = _need_paged(cache, block_table, dev)
     if slot_pos is not None:
-        _want(slot_pos, "slot_pos", torch.int32, (B, 64 * mb), dev)
+        _want(slot_pos, "slot_pos", _i32, (B, 64 * mb), dev)
     ckv_ld, kr_ld = c_kv.stride(0), k_r.stride(0)
     if T <= 1:  # a stride that no second row uses
         ckv_ld, kr_ld = 512, 64
     _check("mla_cache_append_rope", load().mla_cache_append_rope(
         c_kv.data_ptr(), ckv_ld, k_r.data_ptr(), kr_ld, seq_idx.data_ptr(), slot.data_ptr(), pos.data_ptr(), T,
         freqs.data_ptr(), float(mscale), _rope_flags(layout), block_table.data_ptr(), B, mb, NB, cache.data_ptr(),
-        _raw(slot_pos), _stream(stream)))
+        _raw(slot_pos), _handle(stream, dev)))
     return cache
 
 
 def _need_paged(cache, block_table, dev, fp8=False):
     """Checks a paged cache (bf16, or E4M3 codes) and its table; returns (B, max_blocks, num_blocks)."""
-    _want(cache, "cache", torch.uint8 if fp8 else torch.bfloat16, None, dev)
-    if cache.dim() != 3 or cache.shape[1:] != ((64, 512) if fp8 else (64, 576)):
+    _want(cache, "cache", _u8 if fp8 else _bf16, None, dev)
+    if cache.dim() != 3 or cache.size(1) != 64 or cache.size(2) != (512 if fp8 else 576):
         raise ValueError("fp8 cache must be [num_blocks,64,512] uint8" if fp8 else "bf16 cache must be [num_blocks,64,576]")
-    _want(block_table, "block_table", torch.int32, None, dev)
+    _want(block_table, "block_table", _i32, None, dev)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B,max_blocks]")
     B, mb = block_table.shape
-    return B, mb, cache.shape[0]
+    return B, mb, cache.size(0)
 
 
 def mla_chunk_workspace_bytes(T: int, B: int, H: int, num_splits: int = 0) -> int:
@@ -519,10 +531,10 @@ def _need_chunk(q, q_offsets, cache, block_table, seq_lens, dev, fp8=False):
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [T,H,576] tensor")
     T, H, _ = q.shape
-    _want(q, "q", torch.bfloat16, (T, H, 576), dev)
+    _want(q, "q", _bf16, (T, H, 576), dev)
     B, mb, NB = _need_paged(cache, block_table, dev, fp8)
-    _want(q_offsets, "q_offsets", torch.int32, (B + 1,), dev)
-    _want(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    _want(q_offsets, "q_offsets", _i32, (B + 1,), dev)
+    _want(seq_lens, "seq_lens", _i32, (B,), dev)
     return T, H, B, mb, NB
 
 
@@ -535,18 +547,18 @@ def mla_chunk_attend(q, q_offsets, cache, block_table, seq_lens, softmax_scale, 
     fp8 = isinstance(cache, torch.Tensor) and cache.dtype == torch.uint8
     T, H, B, mb, NB = _need_chunk(q, q_offsets, cache, block_table, seq_lens, dev, fp8)
     if fp8:
-        _want(k_rope, "k_rope", torch.bfloat16, (NB, 64, 64), dev)
-        _want(block_scale, "block_scale", torch.float32, (NB,), dev)
+        _want(k_rope, "k_rope", _bf16, (NB, 64, 64), dev)
+        _want(block_scale, "block_scale", _f32, (NB,), dev)
     elif k_rope is not None or block_scale is not None:
         raise ValueError("k_rope and block_scale belong to an fp8 cache")
-    _want(out, "out", torch.bfloat16, (T, H, 512), dev)
-    _want(lse, "lse", torch.float32, (T, H), dev)
-    _want(workspace, "workspace", torch.uint8, None, dev)
+    _want(out, "out", _bf16, (T, H, 512), dev)
+    _want(lse, "lse", _f32, (T, H), dev)
+    _want(workspace, "workspace", _u8, None, dev)
     _check("mla_chunk_attend", load().mla_chunk_attend(
         q.data_ptr(), q_offsets.data_ptr(), T, MLA_CACHE_FP8_E4M3 if fp8 else MLA_CACHE_BF16, cache.data_ptr(),
         _raw(k_rope), _raw(block_scale), block_table.data_ptr(), seq_lens.data_ptr(), B, H, NB, mb,
         float(softmax_scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), int(num_splits),
-        _stream(stream)))
+        _handle(stream, dev)))
     return out, lse
 
 
@@ -556,13 +568,13 @@ def mla_cache_weigh(q, q_offsets, lse, cache, block_table, seq_lens, softmax_sca
     token received from the queries, summed over heads and tokens."""
     dev = torch.cuda.current_device()
     T, H, B, mb, NB = _need_chunk(q, q_offsets, cache, block_table, seq_lens, dev)
-    _want(lse, "lse", torch.float32, (T, H), dev)
+    _want(lse, "lse", _f32, (T, H), dev)
     if weight is not None:
-        _want(weight, "weight", torch.float32, (B, 64 * mb), dev)
-    _want(weight_out, "weight_out", torch.float32, (B, 64 * mb), dev)
+        _want(weight, "weight", _f32, (B, 64 * mb), dev)
+    _want(weight_out, "weight_out", _f32, (B, 64 * mb), dev)
     _check("mla_cache_weigh", load().mla_cache_weigh(
         q.data_ptr(), q_offsets.data_ptr(), T, lse.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
-        seq_lens.data_ptr(), B, H, NB, mb, float(softmax_scale), _raw(weight), weight_out.data_ptr(), _stream(stream)))
+        seq_lens.data_ptr(), B, H, NB, mb, float(softmax_scale), _raw(weight), weight_out.data_ptr(), _handle(stream, dev)))
     return weight_out
 
 
@@ -585,18 +597,18 @@ def mla_cache_evict(weight, slot_pos, seq_lens, keep, n_first, n_recent, block_t
     dev = torch.cuda.current_device()
     B, mb, NB = _need_paged(cache, block_table, dev)
     S = (B, 64 * mb)
-    _want(weight, "weight", torch.float32, S, dev)
-    _want(new_weight, "new_weight", torch.float32, S, dev)
-    _want(slot_pos, "slot_pos", torch.int32, S, dev)
-    _want(new_pos, "new_pos", torch.int32, S, dev)
-    _want(seq_lens, "seq_lens", torch.int32, (B,), dev)
-    _want(keep, "keep", torch.int32, (B,), dev)
-    _want(new_lens, "new_lens", torch.int32, (B,), dev)
-    _want(workspace, "workspace", torch.uint8, None, dev)
+    _want(weight, "weight", _f32, S, dev)
+    _want(new_weight, "new_weight", _f32, S, dev)
+    _want(slot_pos, "slot_pos", _i32, S, dev)
+    _want(new_pos, "new_pos", _i32, S, dev)
+    _want(seq_lens, "seq_lens", _i32, (B,), dev)
+    _want(keep, "keep", _i32, (B,), dev)
+    _want(new_lens, "new_lens", _i32, (B,), dev)
+    _want(workspace, "workspace", _u8, None, dev)
     _check("mla_cache_evict", load().mla_cache_evict(
         weight.data_ptr(), slot_pos.data_ptr(), seq_lens.data_ptr(), keep.data_ptr(), int(n_first), int(n_recent),
         block_table.data_ptr(), B, NB, mb, cache.data_ptr(), new_weight.data_ptr(), new_pos.data_ptr(),
-        new_lens.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(stream)))
+        new_lens.data_ptr(), workspace.data_ptr(), workspace.numel(), _handle(stream, dev)))
     return new_lens, new_weight, new_pos
 
 

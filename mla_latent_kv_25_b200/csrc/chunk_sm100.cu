@@ -1143,20 +1143,11 @@ __device__ T block_scan(T v, T* warp_sums, T* total) {
 }
 
 // The tile list: tiles of up to 256 / H tokens of one sequence, and the
-// running count of the cache blocks they read.  kFew: at most kPlanFew
-// sequences and tiles, whose lists stay in shared memory between the steps
-// (1.4 us instead of 2.1, at the head of every small call).
-template <bool kFew>
-__global__ void __launch_bounds__(kFew ? kPlanFew : kPlanThreads) chunk_plan_kernel(const ChunkParams p) {
+// running count of the cache blocks they read.
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ long long sums[32];
   __shared__ int isums[32];
-  __shared__ int few_off[kFew ? kPlanFew + 1 : 1], few_a[kFew ? kPlanFew : 1], few_n[kFew ? kPlanFew : 1],
-      few_len[kFew ? kPlanFew : 1];
-  __shared__ long long few_pre[kFew ? kPlanFew + 1 : 1];
-  __shared__ int4 few_tile[kFew ? kPlanFew : 1];
-  int* const off = kFew ? few_off : p.tile_off;
-  const long long* const pre = kFew ? few_pre : p.pre;
   const int per = kTileRows / p.H;
   int nt = 0;
   for (int b0 = 0; b0 < p.B; b0 += blockDim.x) {
@@ -1164,32 +1155,26 @@ __global__ void __launch_bounds__(kFew ? kPlanFew : kPlanThreads) chunk_plan_ker
     int tiles = 0;
     if (b < p.B) {
       const int a = p.q_offsets[b], e = p.q_offsets[b + 1];
-      const int len = checked_len(p.seq_lens, b, p.max_blocks, p.err);
+      checked_len(p.seq_lens, b, p.max_blocks, p.err);
       if (a < 0 || e < a || e > p.T)
         atomicOr(p.err, kErrSeqTooLong);
       else
         tiles = (e - a + per - 1) / per;
-      if (kFew) {
-        few_a[b] = a;
-        few_n[b] = e - a;
-        few_len[b] = len;
-      }
     }
     int total;
     const int incl = block_scan(tiles, isums, &total);
     // only offsets that decrease somewhere can ask for more tiles than T
     // tokens fill: what is over is left out
     if (b < p.B) {
-      off[b] = min(p.max_tiles, nt + incl - tiles);
+      p.tile_off[b] = min(p.max_tiles, nt + incl - tiles);
       if (nt + incl > p.max_tiles) atomicOr(p.err, kErrSeqTooLong);
     }
     nt = min(p.max_tiles, nt + total);
   }
   if (threadIdx.x == 0) {
-    off[p.B] = nt;
+    p.tile_off[p.B] = nt;
     *p.n_tiles = nt;
     p.pre[0] = 0;
-    if (kFew) few_pre[0] = 0;
   }
   __syncthreads();
   long long blocks = 0;
@@ -1197,28 +1182,22 @@ __global__ void __launch_bounds__(kFew ? kPlanFew : kPlanThreads) chunk_plan_ker
     const int t = t0 + threadIdx.x;
     long long mine = 0;
     if (t < nt) {
-      int lo = 0, hi = p.B;  // off[lo] <= t < off[hi]
+      int lo = 0, hi = p.B;  // tile_off[lo] <= t < tile_off[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (off[mid] <= t) lo = mid; else hi = mid;
+        if (p.tile_off[mid] <= t) lo = mid; else hi = mid;
       }
-      const int a = kFew ? few_a[lo] : p.q_offsets[lo], n = kFew ? few_n[lo] : p.q_offsets[lo + 1] - a;
-      const int seen = kFew ? few_len[lo] : checked_len(p.seq_lens, lo, p.max_blocks, nullptr);
-      const int j = (t - off[lo]) * per;
+      const int a = p.q_offsets[lo], n = p.q_offsets[lo + 1] - a;
+      const int j = (t - p.tile_off[lo]) * per;
       const int tok = min(per, n - j);
       // the tile's last token sees the sequence without the n - j - tok tokens behind it
-      const int len = max(0, seen - (n - j - tok));
-      const int4 tile = make_int4((a + j) * p.H, tok * p.H, lo, len);
-      p.tiles[t] = tile;
-      if (kFew) few_tile[t] = tile;
+      const int len = max(0, checked_len(p.seq_lens, lo, p.max_blocks, nullptr) - (n - j - tok));
+      p.tiles[t] = make_int4((a + j) * p.H, tok * p.H, lo, len);
       mine = len > 0 ? nblocks_of(len) + kTileUnits : 0;
     }
     long long total;
     const long long incl = block_scan(mine, sums, &total);
-    if (t < nt) {
-      p.pre[t + 1] = blocks + incl;
-      if (kFew) few_pre[t + 1] = blocks + incl;
-    }
+    if (t < nt) p.pre[t + 1] = blocks + incl;
     blocks += total;
   }
   // every engine's range and first tile (t = nt: none)
@@ -1231,10 +1210,10 @@ __global__ void __launch_bounds__(kFew ? kPlanFew : kPlanThreads) chunk_plan_ker
     if (e < P) {
       r.s = range_start(e, blocks, P);
       r.e = range_start(e + 1, blocks, P);
-      r.t = tile_of(pre, nt, r.s);
-      r.a = pre[r.t];
-      r.z = pre[r.t + 1];
-      r.tile = kFew ? few_tile[r.t] : p.tiles[r.t];
+      r.t = tile_of(p.pre, nt, r.s);
+      r.a = p.pre[r.t];
+      r.z = p.pre[r.t + 1];
+      r.tile = p.tiles[r.t];
     }
     p.engines[e] = r;
   }
@@ -1350,10 +1329,8 @@ cudaError_t launch_chunk_sm100(const ChunkParams& p, const ChunkMaps& maps, cuda
     if (cudaError_t e = set_attributes(); e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  if (p.B <= kPlanFew && p.max_tiles <= kPlanFew)
-    chunk_plan_kernel<true><<<1, kPlanFew, 0, stream>>>(p);
-  else
-    chunk_plan_kernel<false><<<1, kPlanThreads, 0, stream>>>(p);
+  const int threads = p.B <= kPlanFew && p.max_tiles <= kPlanFew ? kPlanFew : kPlanThreads;
+  chunk_plan_kernel<<<1, threads, 0, stream>>>(p);
   if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
