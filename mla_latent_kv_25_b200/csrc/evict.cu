@@ -258,21 +258,23 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
 
   for (int i = threadIdx.x; i < (kPasses + 1) * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
 
-  // Keys and the newest position.  Eight loads of each array are in flight
-  // before the copies, which the compiler has to take for writes to them.  Keys
+  // Keys and the newest position.  Four loads of each array are in flight
+  // before the copies, which the compiler has to take for writes to them (16:
+  // slower below 16384 slots a sequence, the same above; all of this kernel's
+  // code runs once, and fetching unrolled loops costs more than they save).  Keys
   // are at least 0x7fffff; 0 stands for a slot that does not compete.
   int last = INT32_MIN;
-  for (int s0 = lo; s0 < hi; s0 += 256) {
-    int ps[8];
-    float ws[8];
+  for (int s0 = lo; s0 < hi; s0 += 128) {
+    int ps[4];
+    float ws[4];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < 4; ++u) {
       const int s = s0 + 32 * u + lane;
       ps[u] = s < hi ? pos[s] : INT32_MIN;
       ws[u] = s < hi ? w[s] : 0.f;
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < 4; ++u) {
       const int s = s0 + 32 * u + lane;
       last = max(last, ps[u]);
       if (kStored && s0 + 32 * u < hi) keys[s - c0] = s < hi ? weight_key(ws[u]) : 0u;
@@ -295,7 +297,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
 
   // protection bits, and the histogram of the top digit of each class
   int guarded_here = 0;
-#pragma unroll 8
+#pragma unroll 4
   for (int s0 = lo; s0 < hi; s0 += 32) {
     const int s = s0 + lane;
     const bool in = s < hi;
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
 #pragma unroll
     for (int pass = 1; pass < kPasses; ++pass) {
       int* hist = sh.hist[1 + pass];
-#pragma unroll 8
+#pragma unroll 4
       for (int s0 = lo; s0 < hi; s0 += 32) {
         const uint32_t key = key_of(s0);
         if ((key >> digit_shift(pass - 1)) == thr) atomicAdd(&hist[(key >> digit_shift(pass)) & digit_mask(pass)], 1);
