@@ -144,9 +144,13 @@ struct Seg {
 // its blocks last.  Without that charge an engine that gets many short tiles
 // takes far longer than one with a single long tile.
 constexpr int kTileUnits = 8;
-// An engine gets at least this many units: fewer engines than that leave the
-// merge less to read than they save.
-constexpr int kMinUnits = 16;
+// An engine gets at least this many units: shorter ranges cost more in the
+// merge than they save (1 x 128 heads over 4096: 31.8 us with 16, 29.6 with 10,
+// 28.6 with 8; over 16384 37.8, 39.8 and 40.5).
+constexpr int kMinUnits = 10;
+// What a range may have above the even share for the tiles to stay whole.
+constexpr int kWholeUnits = 16;
+constexpr int kMaxEngines = 64;  // 148 SMs hold 37 clusters of four
 
 __device__ __forceinline__ int engines_of(const ChunkParams& p, long long total) {
   const long long most = (total + kMinUnits - 1) / kMinUnits;
@@ -1148,6 +1152,9 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ long long sums[32];
   __shared__ int isums[32];
+  __shared__ long long even[kMaxEngines + 1], whole[kMaxEngines + 1];
+  __shared__ int uneven;
+  if (threadIdx.x == 0) uneven = 0;
   const int per = kTileRows / p.H;
   int nt = 0;
   for (int b0 = 0; b0 < p.B; b0 += blockDim.x) {
@@ -1200,16 +1207,54 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
     if (t < nt) p.pre[t + 1] = blocks + incl;
     blocks += total;
   }
-  // every engine's range and first tile (t = nt: none)
+  // Every engine's range and first tile (t = nt: none).  With few tiles to an
+  // engine the even cut at x moves to the nearest end of its tile if that is
+  // at most kTileUnits and a sixteenth of a range away (a piece costs as much),
+  // or everywhere if no range then exceeds the even one by more than kWholeUnits
+  // and half of it: no tile is cut, and there is nothing to merge.  (More than
+  // kMaxEngines, which only a caller can ask for, keep the even cuts.)
+  // Measured, even cuts first: 32 x 4 tokens x 128 heads over 256 44.2 us and
+  // 34.7, 32 x 8 over 2048 142 and 131, 64 x 1 over 4096 127 and 121; a batch
+  // that has to be cut anyway pays up to 1 us.
   __syncthreads();
   const int P = engines_of(p, blocks);
+  const bool move = P > 0 && P <= kMaxEngines && 2 * nt >= P;
+  // 32-bit divisions where they do (64 * 2^26 = 2^32)
+  const bool narrow = P <= kMaxEngines && blocks < (1LL << 26);
+  const long long share = !move ? 0 : narrow ? static_cast<unsigned>(blocks) / static_cast<unsigned>(P) : blocks / P;
+  const long long near = min(static_cast<long long>(kTileUnits), share / 16);
+  const long long slack = min(static_cast<long long>(kWholeUnits), share / 2);
+  auto start_of = [&](int e) -> long long {
+    return narrow ? static_cast<unsigned>(e) * static_cast<unsigned>(blocks) / static_cast<unsigned>(P)
+                  : range_start(e, blocks, P);
+  };
+  if (move) {
+    for (int e = threadIdx.x; e <= P; e += blockDim.x) {
+      long long x = start_of(e), w = x;
+      if (e > 0 && e < P) {
+        const int t = tile_of(p.pre, nt, x);
+        const long long a = p.pre[t], z = p.pre[t + 1];
+        w = x - a <= z - x ? a : z;
+        if (llabs(w - x) <= near) x = w;
+      }
+      even[e] = x;
+      whole[e] = w;
+    }
+    __syncthreads();
+    if (threadIdx.x < kMaxEngines) {
+      const int e = threadIdx.x;
+      if (__any_sync(0xffffffffu, e < P && whole[e + 1] - whole[e] > share + slack) && (e & 31) == 0) uneven = 1;
+    }
+    __syncthreads();
+  }
+  const long long* cut = uneven != 0 ? even : whole;
   for (int e = threadIdx.x; e < p.P; e += blockDim.x) {
     ChunkEngine r = {};
     r.t = r.nt = nt;
     r.total = blocks;
     if (e < P) {
-      r.s = range_start(e, blocks, P);
-      r.e = range_start(e + 1, blocks, P);
+      r.s = move ? cut[e] : start_of(e);
+      r.e = move ? cut[e + 1] : start_of(e + 1);
       r.t = tile_of(p.pre, nt, r.s);
       r.a = p.pre[r.t];
       r.z = p.pre[r.t + 1];
@@ -1257,16 +1302,22 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkP
     for (long long r = wid; r < static_cast<long long>(blind) * p.H; r += kMergeGrid * kMergeWarps)
       fill_row(p, size_t(a) * p.H + r, -INFINITY, lane);
   }
-  const long long total = r.total, x = r.s, a = r.a, z = r.z;
-  const int P = engines_of(p, total);
-  if (e1 >= P) return;
+  if (r.t >= r.nt) return;  // past the last engine
+  const long long x = r.s, a = r.a, z = r.z;
   // merged at the boundary whose left engine holds the tile's first block
   if (x <= a + kTileUnits || s0 > a + kTileUnits) return;
   const int4 info = r.tile;
+  // pieces: one per engine from the left one on whose range starts before the
+  // tile ends (no range inside a tile is empty)
+  int n = 1;
+  for (int e0 = e1; e0 < p.P; e0 += 32) {
+    const bool in = e0 + lane < p.P && p.engines[e0 + lane].t < r.nt && p.engines[e0 + lane].s < z;
+    const unsigned m = __ballot_sync(0xffffffffu, in);
+    n += __popc(m);
+    if (m != 0xffffffffu) break;
+  }
   const int row = (wid & 7) * 32 + lane, col4 = (wid >> 3) * (kMergeCols / 4);
   if (row >= info.y) return;
-  const int last = engine_of(z - 1, total, P);
-  const int n = last - (e1 - 1) + 1;
   // the first piece is its engine's second segment if the engine's range starts in an earlier tile
   auto slot_of = [&](int i) { return 2 * (e1 - 1 + i) + (i == 0 && s0 < a ? 1 : 0); };
   float M = -INFINITY, sum = 0.f;

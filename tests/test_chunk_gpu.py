@@ -54,6 +54,20 @@ def test_chunk_split_counts(num_splits):
     check(Chunk([9, 1, 4], [1000, 63, 300], 64, seed=4), num_splits, what=f"splits={num_splits}")
 
 
+@pytest.mark.parametrize("num_splits", [0, 1, 13, 37, 64, 65])
+@pytest.mark.parametrize("name", ["equal", "ragged", "one_long", "empty"])
+def test_chunk_tiles_that_stay_whole(name, num_splits):
+    """Several tiles to an engine: cuts that move to the ends of tiles, all of them or some, empty
+    ranges, more engines than that is done for, sequences without queries or without a cache."""
+    g = torch.Generator().manual_seed(17)
+    n, lens = {"equal": ([4] * 40, [250] * 40),
+               "ragged": (torch.randint(1, 7, (48,), generator=g).tolist(), torch.randint(8, 700, (48,), generator=g).tolist()),
+               "one_long": ([2] * 30, [5000] + [130] * 29),
+               "empty": ([2, 0, 3, 1, 0] * 8, [100, 50, 0, 300, 0] * 8)}[name]
+    lens = [max(a, b) if b else 0 for a, b in zip(n, lens)]
+    check(Chunk(n, lens, 128, seed=num_splits), num_splits, what=f"{name}, splits={num_splits}")
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
 def test_chunk_scales(scale):
     """Uniform, inverted and sharp softmax."""
