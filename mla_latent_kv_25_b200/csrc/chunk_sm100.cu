@@ -111,7 +111,7 @@ static_assert(sizeof(Barriers) <= 1024, "barrier block too large");
 
 constexpr uint32_t kMaxOff = 1024;             // score: float [2 halves][128] running maxima
 constexpr uint32_t kSumOff = kMaxOff + 1024;   // score: float [2 halves][128] sums
-constexpr uint32_t kQOff = 3072;               // score: the last chunk of Q
+constexpr uint32_t kQOff = kSumOff + 1024;     // score: the last chunk of Q
 __host__ __device__ constexpr uint32_t k_slot_off(int s) { return kQOff + kQChunk + s * kKSlot; }
 __host__ __device__ constexpr uint32_t v_slot_off(int s) { return 1024 + s * kVSlot; }
 __host__ __device__ constexpr uint32_t rec_off(int r) { return 1024 + kVSlots * kVSlot + r * kRecBytes; }
