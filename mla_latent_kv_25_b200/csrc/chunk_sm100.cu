@@ -861,25 +861,26 @@ __device__ __forceinline__ size_t piece_unit(int slot, int col4, int row) {
 // warp fills four whole lines.  The time of a store goes with the lines it
 // touches (measured for a tile's output: 7 us when every lane stores its own
 // row, 2.3-5 us with eight 64-byte pieces a store).  16-byte units are swizzled
-// against bank conflicts.  dst(r) is row r's address, or null for a padding row.
-template <class Dst>
-__device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint4 (&a)[4], const uint4 (&b)[4], Dst dst) {
+// against bank conflicts.  `dst` is where lane l's 16 bytes of row l / 8 go;
+// rows are kDc elements apart, and `rows` of them from that one on exist.
+__device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint4 (&a)[4], const uint4 (&b)[4], uint8_t* dst,
+                                           int rows) {
+  uint8_t* const to = stage + (lane & 15) * 128;
+  const uint8_t* const from = stage + (lane >> 3) * 128;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     __syncwarp();
     if ((lane >> 4) == half) {
-      const int r = lane & 15;
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        *reinterpret_cast<uint4*>(stage + r * 128 + ((q ^ (r & 7)) << 4)) = q < 4 ? a[q & 3] : b[q & 3];
+      for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4*>(to + ((q ^ (lane & 7)) << 4)) = q < 4 ? a[q & 3] : b[q & 3];
     }
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = 4 * i + (lane >> 3), q = lane & 7;
-      uint8_t* at = dst(16 * half + r);
-      if (at != nullptr)
-        *reinterpret_cast<uint4*>(at + 16 * q) = *reinterpret_cast<const uint4*>(stage + r * 128 + ((q ^ (r & 7)) << 4));
+      const int r = 16 * half + 4 * i;  // and lane / 8; swizzled by the row's place in its group of eight
+      if (r < rows)
+        *reinterpret_cast<uint4*>(dst + r * (kDc * 2)) = *reinterpret_cast<const uint4*>(
+            from + 4 * i * 128 + (((lane & 7) ^ ((4 * i + (lane >> 3)) & 7)) << 4));
     }
   }
 }
@@ -942,19 +943,28 @@ __device__ __forceinline__ void value_epilogue(const Ctx& c) {
       const float lse = l_fin == 0.f ? -INFINITY : (m_fin + log2f(l_fin)) * 0.6931471805599453f;
       uint8_t* stage = c.gbase + stage_off(c.warp - 4);
       const int row0 = 128 * (c.rank - 2) + q4 * 32;  // the warp's first row
+      if (!release_record()) return;
+      const bool any_row = row0 < g.rows;  // padding warps only hand O back
       if (g.slot < 0) {
-        if (!release_record()) return;
         // A loop: unrolled, with all of the row's half in registers before the
-        // first store, O is free earlier, but fetching its instructions costs
-        // more (a tile's output 4.1 us against 3.2; calls of many tiles 3 % faster,
-        // small ones 8 % slower).
+        // first store, a tile's output took 4.1 us against 3.2, most of it for
+        // fetching instructions.  The next columns are read while these are
+        // stored, so that O is free two steps before the end (512 tokens over
+        // 512, eight short tiles an engine: 86.6 -> 81.0 us).
+        uint32_t v[2][32];
+        auto read = [&](int ch) {
+          tmem_ld32(c.tmem + lane_off + ocol + 32 * ch, v[0]);
+          tmem_ld32(c.tmem + lane_off + ocol + 32 * ch + 32, v[1]);
+        };
+        uint8_t* const out = reinterpret_cast<uint8_t*>(p.out + (size_t(g.row0) + row0 + (c.lane >> 3)) * kDc) + 16 * (c.lane & 7);
+        const int rows = g.rows - row0 - (c.lane >> 3);
+        if (any_row) {
+          read(0);
+          tmem_ld_wait();
+        }
 #pragma unroll 1
         for (int ch = 0; ch < 8; ch += 2) {
           uint4 o[2][4];
-          uint32_t v[2][32];
-          tmem_ld32(c.tmem + lane_off + ocol + 32 * ch, v[0]);
-          tmem_ld32(c.tmem + lane_off + ocol + 32 * ch + 32, v[1]);
-          tmem_ld_wait();
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -969,21 +979,20 @@ __device__ __forceinline__ void value_epilogue(const Ctx& c) {
               o[k][q] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
             }
           }
-          if (ch == 6) {
+          if (ch < 6 && any_row) read(ch + 2);
+          if (ch == 4 || !any_row) {  // the last columns are in registers
+            tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
             if (c.lane == 0) mbar_arrive_cluster_relaxed(o_free);
           }
-          const int col = latent_of(ocol + 32 * ch);
-          store_rows(stage, c.lane, o[0], o[1], [&](int r) -> uint8_t* {
-            if (row0 + r >= g.rows) return nullptr;
-            return reinterpret_cast<uint8_t*>(p.out + (size_t(g.row0) + row0 + r) * kDc + col);
-          });
+          if (!any_row) break;
+          store_rows(stage, c.lane, o[0], o[1], out + 2 * latent_of(ocol + 32 * ch), rows);
+          if (ch < 4) tmem_ld_wait();
         }
       } else {
-        if (!release_record()) return;
 #pragma unroll 1
-        for (int ch = 0; ch < 8; ++ch) {
+        for (int ch = 0; any_row && ch < 8; ++ch) {
           __syncwarp();
           uint32_t v[32];
           tmem_ld32(c.tmem + lane_off + ocol + 32 * ch, v);
