@@ -1227,7 +1227,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   // that has to be cut anyway pays up to 1 us.
   __syncthreads();
   const int P = engines_of(p, blocks);
-  const bool move = P > 0 && P <= kMaxEngines && 2 * nt >= P;
+  const bool move = P > 1 && P <= kMaxEngines && nt > 1 && 2 * nt >= P;
   // 32-bit divisions where they do (64 * 2^26 = 2^32)
   const bool narrow = P <= kMaxEngines && blocks < (1LL << 26);
   const long long share = !move ? 0 : narrow ? static_cast<unsigned>(blocks) / static_cast<unsigned>(P) : blocks / P;
