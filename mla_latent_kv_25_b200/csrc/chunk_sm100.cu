@@ -1381,7 +1381,7 @@ int chunk_sm100_max_clusters() {
   return n;
 }
 
-cudaError_t launch_chunk_sm100(const ChunkParams& p, const ChunkMaps& maps, cudaStream_t stream) {
+cudaError_t launch_chunk_sm100(const ChunkParams& given, const ChunkMaps& maps, cudaStream_t stream) {
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -1389,6 +1389,10 @@ cudaError_t launch_chunk_sm100(const ChunkParams& p, const ChunkMaps& maps, cuda
     if (cudaError_t e = set_attributes(); e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
+  // no more engines than the table's width could fill with kMinUnits each
+  const long long most = (static_cast<long long>(given.max_tiles) * (given.max_blocks + kTileUnits) + kMinUnits - 1) / kMinUnits;
+  ChunkParams p = given;
+  if (most < p.P) p.P = most > 0 ? static_cast<int>(most) : 1;
   const int threads = p.B <= kPlanFew && p.max_tiles <= kPlanFew ? kPlanFew : kPlanThreads;
   chunk_plan_kernel<<<1, threads, 0, stream>>>(p);
   if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
