@@ -479,8 +479,12 @@ size_t mla_evict_workspace_bytes(int B, int max_blocks_per_seq);
  * compacted for all its sequences).
  * max_blocks_per_seq: at most 65536 (MLA_ERR_UNSUPPORTED above).
  * workspace: mla_evict_workspace_bytes(...), 256-byte aligned, zero-filled before its
- * first use, one call at a time; error bits by mla_get_device_error (a row whose source
- * or destination has a bad block id is not moved).
+ * first use, one call at a time; error bits by mla_get_device_error.  A token whose row
+ * cannot move, because its source or destination slot has a bad block id
+ * (MLA_DEVERR_BAD_BLOCK) or a wait gave up (MLA_DEVERR_TIMEOUT), stays where it was: its
+ * slot, at or past n, has its row and in new_weight and new_pos its weight and position,
+ * and the slot below n that waited for it keeps its old row and has weight 0 and position
+ * -1.  All other tokens and new_lens are as in a call without errors.
  */
 mla_status_t mla_cache_evict(const float *weight, const int32_t *slot_pos,
                              const int32_t *seq_lens, const int32_t *keep, int n_first,
@@ -503,9 +507,9 @@ mla_status_t mla_cache_get_error(void *stream, uint32_t *err_bits);
  * seconds of SM clock; cycles <= 0 restores the default).  Returns the
  * previous bound.  A wait that reaches the bound records MLA_DEVERR_TIMEOUT,
  * makes every role of the kernel leave its loop, lets copies in flight land
- * and exits; the outputs of that launch are then undefined (mla_decode writes
- * them as out = 0, lse = NaN while the bit is set), the context stays
- * usable.  Meant for tests of that failure path and for diagnosis.
+ * and exits; the outputs of that launch are then undefined (mla_decode and
+ * mla_chunk_attend write them as out = 0, lse = NaN while the bit is set,
+ * mla_cache_evict leaves every token whole), the context stays usable.  Meant for tests of that failure path and for diagnosis.
  */
 long long mla_set_wait_limit(long long cycles);
 

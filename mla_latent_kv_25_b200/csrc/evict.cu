@@ -19,7 +19,7 @@
 //   131072 (eight CTAs each) 56,000, with six cluster barriers and the
 //   instructions of passes over 16 slots per thread.
 // evict_move_kernel: bulk copies of whole rows through shared memory, 32 rows
-//   in flight per warp, and with each row its weight and position.  Bound: HBM,
+//   in flight per warp, and behind each row its weight and position.  Bound: HBM,
 //   2304 bytes per moved row.
 // Whole call: 64 x 4096 -> 2048 38.4 us, 4 x 131072 -> 65536 86 us (rows alone
 // at the measured copy bandwidth: 23.5 and 47).
@@ -493,61 +493,82 @@ __global__ void __launch_bounds__(32) evict_move_kernel(const EvictParams p) {
   const int32_t* table = p.block_table + size_t(b) * p.max_blocks;
   int abort = 0;
   const WaitCtx wc{p.spin_limit, p.err, &abort};
-  void* dst[kMoveStages] = {nullptr, nullptr};
   const size_t at = size_t(b) * p.max_blocks * kBlock;
   const float* w = p.weight + at;
   const int32_t* pos = p.slot_pos + at;
   float* nw = p.new_weight + at;
   int32_t* np = p.new_pos + at;
-  auto load = [&](int step, int st) {
+  // this lane's move of a step: its slots (x < 0: none), their values, and
+  // where the row goes (null: a block id is bad)
+  struct Move {
+    int2 m;
+    float w;
+    int pos;
+    void* dst;
+  };
+  auto read = [&](int step, const __nv_bfloat16** src) {
     const int k = lane < kMoveRows ? step * kMoveRows + lane : n;
-    const __nv_bfloat16* src = nullptr;
-    dst[st] = nullptr;
-    float ws = 0.f;
-    int ps = 0;
-    int2 m = make_int2(0, 0);
-    if (k < n) {
-      m = moves[k];
-      ws = w[m.x];
-      ps = pos[m.x];
-      const int sb = table[m.x / kBlock], db = table[m.y / kBlock];
-      if (sb < 0 || sb >= p.num_blocks || db < 0 || db >= p.num_blocks) {
-        atomicOr(p.err, kErrBadBlock);
-      } else {
-        src = p.cache + (size_t(sb) * kBlock + m.x % kBlock) * kRow;
-        dst[st] = p.cache + (size_t(db) * kBlock + m.y % kBlock) * kRow;
-      }
+    Move v = {make_int2(-1, -1), 0.f, 0, nullptr};
+    *src = nullptr;
+    if (k >= n) return v;
+    v.m = moves[k];
+    v.w = w[v.m.x];
+    v.pos = pos[v.m.x];
+    const int sb = table[v.m.x / kBlock], db = table[v.m.y / kBlock];
+    if (sb < 0 || sb >= p.num_blocks || db < 0 || db >= p.num_blocks) {
+      atomicOr(p.err, kErrBadBlock);
+    } else {
+      *src = p.cache + (size_t(sb) * kBlock + v.m.x % kBlock) * kRow;
+      v.dst = p.cache + (size_t(db) * kBlock + v.m.y % kBlock) * kRow;
     }
+    return v;
+  };
+  auto load = [&](int step, int st) {
+    const __nv_bfloat16* src;
+    const Move v = read(step, &src);
     const uint32_t bar = smem_u32(&full[st]);
     const int rows_in = __popc(__ballot_sync(0xffffffffu, src != nullptr));
     if (lane == 0) mbar_arrive_expect_tx(bar, rows_in * kRowBytes);
     __syncwarp();
     if (src != nullptr) bulk_load(smem_u32(rows) + (st * kMoveRows + lane) * kRowBytes, src, kRowBytes, bar);
-    if (k < n) {  // no other move reads or writes these slots: in place is safe
-      nw[m.y] = ws;
-      np[m.y] = ps;
-      nw[m.x] = 0.f;
-      np[m.x] = -1;
-    }
+    return v;
   };
-  load(blockIdx.x, 0);
+  // The values follow a row once it has landed; a token whose row does not
+  // move stays in its slot with them, and the slot that waited for it is
+  // marked empty.  No other move reads or writes these slots: in place is safe.
+  auto publish = [&](const Move& v, bool moved) {
+    if (v.m.x < 0) return;
+    nw[v.m.y] = moved ? v.w : 0.f;
+    np[v.m.y] = moved ? v.pos : -1;
+    nw[v.m.x] = moved ? 0.f : v.w;
+    np[v.m.x] = moved ? -1 : v.pos;
+  };
+  const int stride = gridDim.x;
+  Move now = load(blockIdx.x, 0);
   uint32_t it = 0;
-  for (int step = blockIdx.x; step < steps; step += gridDim.x, ++it) {
+  for (int step = blockIdx.x; step < steps; step += stride, ++it) {
     const int st = it & 1;
-    if (step + static_cast<int>(gridDim.x) < steps) {
+    Move next = {make_int2(-1, -1), 0.f, 0, nullptr};
+    if (step + stride < steps) {
       // the other stage's stores have read their rows
       asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       __syncwarp();
-      load(step + gridDim.x, st ^ 1);
+      next = load(step + stride, st ^ 1);
     }
     if (!warp_wait(smem_u32(&full[st]), (it >> 1) & 1u, wc)) {
+      publish(now, false);
+      publish(next, false);
+      const __nv_bfloat16* src;
+      for (int s = step + 2 * stride; s < steps; s += stride) publish(read(s, &src), false);
       // loads still in flight land before the CTA exits
       const long long t0 = clock64();
       while (clock64() - t0 < 20000000LL) __nanosleep(1000);
       return;
     }
-    if (dst[st] != nullptr) bulk_store(dst[st], smem_u32(rows) + (st * kMoveRows + lane) * kRowBytes, kRowBytes);
+    if (now.dst != nullptr) bulk_store(now.dst, smem_u32(rows) + (st * kMoveRows + lane) * kRowBytes, kRowBytes);
+    publish(now, now.dst != nullptr);
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    now = next;
   }
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
