@@ -308,12 +308,9 @@ mla_status_t mla_cache_quantize_fp8(const void* cache_bf16, const int32_t* block
 mla_status_t mla_cache_get_error(void* stream, uint32_t* err_bits) {
   if (!err_bits) return MLA_ERR_INVALID_ARG;
   uint32_t v = 0;
-  uint32_t w = 0;
   if (cudaError_t e = cache_take_error(&v, static_cast<cudaStream_t>(stream)); e != cudaSuccess)
     return cuda_fail(e);
-  if (cudaError_t e = weigh_take_error(&w, static_cast<cudaStream_t>(stream)); e != cudaSuccess)
-    return cuda_fail(e);
-  *err_bits = v | w;
+  *err_bits = v;
   return MLA_OK;
 }
 
@@ -725,6 +722,7 @@ mla_status_t mla_cache_weigh(const void* q, const int32_t* q_offsets, int T, con
   p.softmax_scale = softmax_scale;
   p.weight_in = weight_in;
   p.weight_out = weight_out;
+  if (cudaError_t e = cache_error_word(&p.err); e != cudaSuccess) return cuda_fail(e);
   p.spin_limit = g_decode_wait_limit.load();
   CUtensorMap qmap, kmap;
   // without queries the map is never read through: any valid base does

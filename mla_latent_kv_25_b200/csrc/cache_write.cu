@@ -28,8 +28,9 @@
 
 namespace mla {
 
-// Error word of the cache writers (the calls have no workspace): bad block
-// ids and positions outside the table.  Read and cleared by mla_cache_get_error.
+// Error word of the calls on the cache that have no workspace (the writers here
+// and mla_cache_weigh, which gets its address from cache_error_word): one word,
+// so that mla_cache_get_error reads and clears it in one go.
 __device__ uint32_t g_cache_err;
 
 namespace {
@@ -187,9 +188,13 @@ cudaError_t launch_cache_quantize_fp8(const __nv_bfloat16* cache_bf16, const int
   return cudaGetLastError();
 }
 
+cudaError_t cache_error_word(uint32_t** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_cache_err);
+}
+
 cudaError_t cache_take_error(uint32_t* bits, cudaStream_t stream) {
   uint32_t* dev = nullptr;
-  cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void**>(&dev), g_cache_err);
+  cudaError_t e = cache_error_word(&dev);
   if (e != cudaSuccess) return e;
   if ((e = cudaMemcpyAsync(bits, dev, sizeof(uint32_t), cudaMemcpyDeviceToHost, stream)) != cudaSuccess)
     return e;

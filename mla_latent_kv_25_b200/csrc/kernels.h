@@ -160,14 +160,13 @@ struct WeighParams {
   float softmax_scale;
   const float* weight_in;  // [B, 64*max_blocks] or null
   float* weight_out;
+  uint32_t* err;           // the cache writers' error word
   long long spin_limit;
 };
 // qmap: q as [T*H, 576]; kmap: the cache as [num_blocks*64, 576]; both with
 // 64 x 64 boxes, 128-byte swizzled.
 cudaError_t launch_weigh(const WeighParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
                          cudaStream_t stream);
-// Copies mla_cache_weigh's error word to *bits and clears it (synchronises `stream`).
-cudaError_t weigh_take_error(uint32_t* bits, cudaStream_t stream);
 
 struct EvictParams {
   const float* weight;      // [B, 64*max_blocks]
@@ -188,6 +187,8 @@ struct EvictParams {
 };
 cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t stream);
 
+// Address of the cache writers' error word on the current device.
+cudaError_t cache_error_word(uint32_t** word);
 // Copies the cache writers' error word to *bits and clears it (synchronises `stream`).
 cudaError_t cache_take_error(uint32_t* bits, cudaStream_t stream);
 // Copies the absorption kernels' error word to *bits and clears it (synchronises `stream`).

@@ -41,11 +41,6 @@
 #include "sm100.cuh"
 
 namespace mla {
-
-// Error word of mla_cache_weigh (the call has no workspace); read and cleared
-// by mla_cache_get_error.
-__device__ uint32_t g_weigh_err;
-
 namespace {
 
 using namespace sm100;
@@ -378,7 +373,7 @@ __device__ __forceinline__ bool accumulate(const Ctx& c, const Segment& g, const
     if (tok < g.len && j + (row >> 6) < g.blk_hi) {
       const int id = p.block_table[size_t(g.b) * p.max_blocks + tok / kBlock];
       const bool ok = id >= 0 && id < p.num_blocks;
-      if (!ok && (row & 63) == 0) atomicOr(&g_weigh_err, kErrBadBlock);
+      if (!ok && (row & 63) == 0) atomicOr(p.err, kErrBadBlock);
       const size_t at = g.b * S + tok;
       const float w = p.weight_in != nullptr ? p.weight_in[at] : 0.f;
       p.weight_out[at] = ok ? w + total : w;
@@ -427,7 +422,7 @@ weigh_sm100_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
   c.base = base;
   c.bars = bars;
   c.tmem = bars->tmem_base;
-  c.wc = WaitCtx{p.spin_limit, &g_weigh_err, &bars->abort};
+  c.wc = WaitCtx{p.spin_limit, p.err, &bars->abort};
   const uint32_t in_cluster = cluster_ctarank();
   c.rank = static_cast<int>(in_cluster & 1u);
   c.lead = in_cluster & ~1u;
@@ -439,16 +434,16 @@ weigh_sm100_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
 
   if (blockIdx.x == 0)  // bad lengths and offsets, once
     for (int b = threadIdx.x; b < p.B; b += kThreads) {
-      checked_len(p.seq_lens, b, p.max_blocks, &g_weigh_err);
+      checked_len(p.seq_lens, b, p.max_blocks, p.err);
       if (p.q_offsets[b] < 0 || p.q_offsets[b + 1] < p.q_offsets[b] || p.q_offsets[b + 1] > p.T)
-        atomicOr(&g_weigh_err, kErrSeqTooLong);
+        atomicOr(p.err, kErrSeqTooLong);
     }
 
   SegWalker w;
   w.init(p.seq_lens, p.B, p.max_blocks, gridDim.x / (2 * pairs), blockIdx.x / (2 * pairs));
   // swizzled tiles need 1024-byte aligned shared memory
   if ((base & 1023u) != 0) {
-    if (threadIdx.x == 0) atomicOr(&g_weigh_err, kErrTimeout);
+    if (threadIdx.x == 0) atomicOr(p.err, kErrTimeout);
     w.b = p.B;  // no segments
   }
   Segment gs;
@@ -550,15 +545,6 @@ cudaError_t launch_weigh(const WeighParams& p, const CUtensorMap& qmap, const CU
   if (qtiles <= 1 && tiles < n) n = tiles > 0 ? tiles : 1;
   cfg.gridDim = dim3((2u << best) * static_cast<unsigned>(n));
   return cudaLaunchKernelEx(&cfg, weigh_sm100_kernel, qmap, kmap, p, 1 << best);
-}
-
-cudaError_t weigh_take_error(uint32_t* bits, cudaStream_t stream) {
-  uint32_t* dev = nullptr;
-  cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void**>(&dev), g_weigh_err);
-  if (e != cudaSuccess) return e;
-  if ((e = cudaMemcpyAsync(bits, dev, sizeof(uint32_t), cudaMemcpyDeviceToHost, stream)) != cudaSuccess) return e;
-  if ((e = cudaMemsetAsync(dev, 0, sizeof(uint32_t), stream)) != cudaSuccess) return e;
-  return cudaStreamSynchronize(stream);
 }
 
 }  // namespace mla
