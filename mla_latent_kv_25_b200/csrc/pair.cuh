@@ -116,7 +116,7 @@ __device__ __forceinline__ bool spin_phase(uint32_t bar, uint32_t parity, const 
 // Arrive on a barrier of any CTA of the cluster (cluster address) without
 // releasing earlier writes: a release at cluster scope costs 0.5 us here
 // (measured: producers that arrived with one issued a 16 KB load per 0.6 us),
-// so hand-offs that publish no generic-proxy write do without.
+// so hand-offs of TMEM, which tcgen05 fences order, do without.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
