@@ -421,7 +421,9 @@ size_t mla_chunk_fp8_workspace_bytes(int T, int B, int H, int max_blocks_per_seq
  * cache is widened to bf16 rows for the whole batch first; MLA_ERR_WORKSPACE_TOO_SMALL
  * with less).  A sequence whose offsets decrease or leave 0..T records
  * MLA_DEVERR_SEQ_TOO_LONG and its tokens are not written.  A cached row that is not finite
- * affects the tokens that see it only.
+ * affects the tokens that see it only: where its score is NaN or +inf, out and lse are NaN;
+ * where it is -inf, the row has probability 0 and out and lse are those without it, but the
+ * columns of out in which the row is infinite may be NaN.
  * T >= 0 (0 is a no-op), T * H <= 2^30.
  */
 mla_status_t mla_chunk_attend(const void *q, const int32_t *q_offsets, int T,

@@ -714,10 +714,12 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t two) {
 
 // Rows past the tile's length are zeroed, so that whatever the cache holds
 // there (even NaN) contributes exactly 0 * 0.  Rows that the tile's last
-// token sees and its first does not lose their infinities and NaN: a token
-// that sees such a row has NaN or infinite scores, hence NaN probabilities,
-// and gets its NaN from those, while one that does not see it (P = 0) must
-// not meet 0 * NaN.
+// token sees and its first does not lose their infinities and NaN, because a
+// token that does not see such a row (P = 0) must not meet 0 * NaN.  One that
+// sees it loses nothing that counts: with a NaN or +inf score its probability
+// is NaN, and so is all of its output; with a -inf score its probability is 0
+// and the row drops out, except that in rows which every token sees, and which
+// are not searched for infinities here, 0 * inf makes the infinite columns NaN.
 __device__ __forceinline__ void value_fixup(const Ctx& c) {
   const ChunkParams& p = *c.p;
   Walker w;
