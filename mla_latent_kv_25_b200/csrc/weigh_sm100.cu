@@ -106,10 +106,14 @@ __device__ __forceinline__ Queries queries_of(const WeighParams& p, int b) {
   return q;
 }
 
-// Rows of query tile i: a multiple of 16, half of them from each CTA.
+// Rows of query tile i: a multiple of 16.
 __device__ __forceinline__ int tile_rows(const Queries& q, int i) {
   return q.stay ? q.rows : min(kStreamRows, q.rows - kStreamRows * i);
 }
+// Rows that its MMAs take, half of them from each CTA.  With cta_group::2 N is a
+// multiple of 32: behind the tile up to 16 rows of other tokens (or zeros) are
+// multiplied and not looked at.
+__device__ __forceinline__ int mma_rows(const Queries& q, int i) { return (tile_rows(q, i) + 31) & ~31; }
 
 struct Ctx {
   const WeighParams* p;
@@ -182,7 +186,7 @@ __device__ __forceinline__ bool produce(const Ctx& c, const CUtensorMap* qmap, c
   auto load_queries = [&]() {
     if (!resident(kChunks * kHalf)) return false;
     for (int ch = 0; ch < kChunks; ++ch)
-      pair_tma_load_2d(c.base + kResOff + ch * kHalf, qmap, 64 * ch, q.row0 + c.rank * (q.rows / 2), res_bar);
+      pair_tma_load_2d(c.base + kResOff + ch * kHalf, qmap, 64 * ch, q.row0 + c.rank * (mma_rows(q, 0) / 2), res_bar);
     return true;
   };
   // The next sequence's queries have to wait for all of the previous one's
@@ -203,7 +207,7 @@ __device__ __forceinline__ bool produce(const Ctx& c, const CUtensorMap* qmap, c
       }
     }
     for (int i = c.pair; i < q.tiles; i += active) {
-      const int row = q.row0 + kStreamRows * i + c.rank * (tile_rows(q, i) / 2);
+      const int row = q.row0 + kStreamRows * i + c.rank * (mma_rows(q, i) / 2);
       const int r0 = q.stay ? y0 : row, r1 = q.stay ? y1 : row + 64;
 #pragma unroll 1
       for (int x = 0; x < 64 * kChunks; x += 64) {
@@ -246,7 +250,7 @@ __device__ __forceinline__ bool multiply(const Ctx& c, int tiles, const Queries&
     if (!q.stay && !wait_resident()) return false;
     for (int i = c.pair; i < q.tiles; i += active, ++ait) {
       const int buf = ait % kAcc;
-      const uint32_t idesc = idesc_bf16(256, tile_rows(q, i), false, false);
+      const uint32_t idesc = idesc_bf16(256, mma_rows(q, i), false, false);
       const uint32_t d = c.tmem + 256 * buf;
       if (!wait_phase(bar_addr(bars->acc_empty[buf]), ((ait / kAcc) & 1u) ^ 1u, c.wc)) return false;
       tc_fence_after();
