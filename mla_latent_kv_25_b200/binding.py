@@ -425,6 +425,14 @@ def _want_rows(t, name, dim, width, dev):
     raise ValueError(f"{name}: the last axis must be contiguous")
 
 
+def _int(v, name):
+    """A whole number that fits the C entry points' int (ctypes would cut it to its low 32 bits)."""
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name}: {v} does not fit 32 bits")
+    return v
+
+
 def _raw(t):
     return None if t is None else t.data_ptr()
 
@@ -442,7 +450,7 @@ def mla_rope_freqs(rot=64, base=10000.0, scaling="none", factor=1.0, orig_len=40
     if scaling not in ROPE_SCALING:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALING)}, got {scaling!r}")
     host = (ctypes.c_double * max(1, int(rot) // 2))()
-    _check("mla_rope_freqs", load().mla_rope_freqs(int(rot), float(base), ROPE_SCALING[scaling], float(factor),
+    _check("mla_rope_freqs", load().mla_rope_freqs(_int(rot, "rot"), float(base), ROPE_SCALING[scaling], float(factor),
                                                    float(orig_len), float(beta_fast), float(beta_slow), host))
     return torch.tensor(list(host), dtype=torch.float64, device=device)
 
@@ -488,7 +496,7 @@ def mla_cache_append_rope(c_kv, k_r, seq_idx, slot, pos, freqs, block_table, cac
     if T <= 1:  # a stride that no second row uses
         ckv_ld, kr_ld = 512, 64
     _check("mla_cache_append_rope", load().mla_cache_append_rope(
-        c_kv.data_ptr(), ckv_ld, k_r.data_ptr(), kr_ld, seq_idx.data_ptr(), slot.data_ptr(), pos.data_ptr(), T,
+        c_kv.data_ptr(), _int(ckv_ld, "c_kv's row stride"), k_r.data_ptr(), _int(kr_ld, "k_r's row stride"), seq_idx.data_ptr(), slot.data_ptr(), pos.data_ptr(), T,
         freqs.data_ptr(), float(mscale), _rope_flags(layout), block_table.data_ptr(), B, mb, NB, cache.data_ptr(),
         _raw(slot_pos), _handle(stream, dev)))
     return cache
@@ -507,11 +515,12 @@ def _need_paged(cache, block_table, dev, fp8=False):
 
 
 def mla_chunk_workspace_bytes(T: int, B: int, H: int, num_splits: int = 0) -> int:
-    return int(load().mla_chunk_workspace_bytes(int(T), int(B), int(H), int(num_splits)))
+    return int(load().mla_chunk_workspace_bytes(_int(T, "T"), _int(B, "B"), _int(H, "H"), _int(num_splits, "num_splits")))
 
 
 def mla_chunk_fp8_workspace_bytes(T: int, B: int, H: int, max_blocks: int, num_splits: int = 0) -> int:
-    return int(load().mla_chunk_fp8_workspace_bytes(int(T), int(B), int(H), int(max_blocks), int(num_splits)))
+    return int(load().mla_chunk_fp8_workspace_bytes(_int(T, "T"), _int(B, "B"), _int(H, "H"), _int(max_blocks, "max_blocks"),
+                                                    _int(num_splits, "num_splits")))
 
 
 def alloc_chunk_workspace(T: int, B: int, H: int, num_splits: int = 0, device=None,
@@ -557,8 +566,8 @@ def mla_chunk_attend(q, q_offsets, cache, block_table, seq_lens, softmax_scale, 
     _check("mla_chunk_attend", load().mla_chunk_attend(
         q.data_ptr(), q_offsets.data_ptr(), T, MLA_CACHE_FP8_E4M3 if fp8 else MLA_CACHE_BF16, cache.data_ptr(),
         _raw(k_rope), _raw(block_scale), block_table.data_ptr(), seq_lens.data_ptr(), B, H, NB, mb,
-        float(softmax_scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), int(num_splits),
-        _handle(stream, dev)))
+        float(softmax_scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        _int(num_splits, "num_splits"), _handle(stream, dev)))
     return out, lse
 
 
@@ -579,7 +588,7 @@ def mla_cache_weigh(q, q_offsets, lse, cache, block_table, seq_lens, softmax_sca
 
 
 def mla_evict_workspace_bytes(B: int, max_blocks: int) -> int:
-    return int(load().mla_evict_workspace_bytes(int(B), int(max_blocks)))
+    return int(load().mla_evict_workspace_bytes(_int(B, "B"), _int(max_blocks, "max_blocks")))
 
 
 def alloc_evict_workspace(B: int, max_blocks: int, device=None) -> torch.Tensor:
@@ -606,8 +615,8 @@ def mla_cache_evict(weight, slot_pos, seq_lens, keep, n_first, n_recent, block_t
     _want(new_lens, "new_lens", _i32, (B,), dev)
     _want(workspace, "workspace", _u8, None, dev)
     _check("mla_cache_evict", load().mla_cache_evict(
-        weight.data_ptr(), slot_pos.data_ptr(), seq_lens.data_ptr(), keep.data_ptr(), int(n_first), int(n_recent),
-        block_table.data_ptr(), B, NB, mb, cache.data_ptr(), new_weight.data_ptr(), new_pos.data_ptr(),
+        weight.data_ptr(), slot_pos.data_ptr(), seq_lens.data_ptr(), keep.data_ptr(), _int(n_first, "n_first"),
+        _int(n_recent, "n_recent"), block_table.data_ptr(), B, NB, mb, cache.data_ptr(), new_weight.data_ptr(), new_pos.data_ptr(),
         new_lens.data_ptr(), workspace.data_ptr(), workspace.numel(), _handle(stream, dev)))
     return new_lens, new_weight, new_pos
 
