@@ -146,8 +146,10 @@ struct Seg {
 // takes far longer than one with a single long tile.
 constexpr int kTileUnits = 8;
 // An engine gets at least this many units: shorter ranges cost more in the
-// merge than they save (1 x 128 heads over 4096: 31.8 us with 16, 29.6 with 10,
-// 28.6 with 8; over 16384 37.8, 39.8 and 40.5).
+// merge than they save.  With 8, 10 and 16 (captured runs, us): 5 x 16 heads over
+// 261 (cut in two, two and one) 19.1, 19.1, 19.3; 1 x 16 over 1000 20.2, 20.1,
+// 22.8; ragged 4 x 3 x 32 over 2000 24.8, 25.3, 29.0; 1 x 128 over 4096 26.2,
+// 27.3, 29.7; over 16384 40.1, 39.0, 37.1; 1 x 16 over 65536 56.0, 55.7, 56.0.
 constexpr int kMinUnits = 10;
 // What a range may have above the even share for the tiles to stay whole.
 constexpr int kWholeUnits = 16;
@@ -1240,6 +1242,11 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   // or everywhere if no range then exceeds the even one by more than kWholeUnits
   // and half of it: no tile is cut, and there is nothing to merge.  (More than
   // kMaxEngines, which only a caller can ask for, keep the even cuts.)
+  // No cut may reach the end of the last tile: the merge finds a cut's tile by
+  // the cut, and there is none behind the last.  The even ones cannot (a range
+  // is longer than a sixteenth of one).  With the others it takes a last tile of
+  // two ranges at least, whose own range is then longer than one and a half: the
+  // even cuts stay.  So `slack` must not exceed half a range.
   // Measured, even cuts first: 32 x 4 tokens x 128 heads over 256 44.2 us and
   // 34.7, 32 x 8 over 2048 142 and 131, 64 x 1 over 4096 127 and 121; a batch
   // that has to be cut anyway pays up to 1 us.
@@ -1278,7 +1285,6 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   for (int e = threadIdx.x; e < p.P; e += blockDim.x) {
     ChunkEngine r = {};
     r.t = r.nt = nt;
-    r.total = blocks;
     if (e < P) {
       r.s = move ? cut[e] : start_of(e);
       r.e = move ? cut[e + 1] : start_of(e + 1);

@@ -112,7 +112,6 @@ struct __align__(16) ChunkEngine {
   int4 tile;             // the first tile's entry of the list
   long long a, z;        // and its units
   long long s, e;        // range
-  long long total;       // units of all tiles
   int t, nt;             // first tile, number of tiles
 };
 
@@ -140,12 +139,11 @@ struct ChunkParams {
   float* lse_part;     // [2P][256]
   float* o_part;       // [2P][512/4][256][4]
 };
-// Plan, attention and merge kernels.  kmap as for launch_weigh; qmap: q as
-// [T*H, 576] with 64 x 128 boxes.
 struct ChunkMaps {
-  CUtensorMap q;          // query rows, boxes of 128 rows x 64 columns
+  CUtensorMap q;          // query rows [T*H, 576], boxes of 128 rows x 64 columns
   CUtensorMap k, k2, k4;  // the cache: one, two and four 64-column chunks of 64 rows
 };
+// Plan, attention and merge kernels.
 cudaError_t launch_chunk_sm100(const ChunkParams& p, const ChunkMaps& maps, cudaStream_t stream);
 int chunk_sm100_max_clusters();
 
