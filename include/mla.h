@@ -321,8 +321,10 @@ mla_status_t mla_cache_quantize_fp8(const void *cache_bf16, const int32_t *block
  *   MLA_ROPE_YARN    pairs that turn more than beta_fast times over the original
  *                    context orig_len keep theta_i, pairs that turn fewer than
  *                    beta_slow times get theta_i / factor, with a linear ramp between
- *                    ("YaRN: Efficient Context Window Extension of Large Language
- *                    Models", NTK-by-parts): with pair(n) = rot * ln(orig_len /
+ *                    (NTK-by-parts of "YaRN: Efficient Context Window Extension of
+ *                    Large Language Models", but with the ramp over the pair index
+ *                    between whole bounds, as released models have it, where the
+ *                    paper's is over the turns): with pair(n) = rot * ln(orig_len /
  *                    (2 pi n)) / (2 ln base), lo = max(0, floor(pair(beta_fast))),
  *                    hi = min(rot - 1, ceil(pair(beta_slow))), r_i = clamp((i - lo) /
  *                    max(hi - lo, 0.001), 0, 1):
@@ -359,8 +361,8 @@ mla_status_t mla_rope_freqs(int rot, double base, mla_rope_scaling_t scaling, do
  * are not touched.  y = x with equal strides rotates in place; y must not overlap x in
  * any other way, nor two of its own rows each other.
  * pos: int32 [T] (any value); freqs: f64 [rot/2] from mla_rope_freqs, on the device;
- * mscale: finite.  The angle is formed and reduced in double, so far positions keep
- * their accuracy; the rotation is fp32, rounded once.  The inverse rotation with the
+ * mscale: finite.  The angle is formed and reduced in double (off by at most 2^-30 turns up
+ * to position 2^24 and 2^-23 at 2^31); the rotation is fp32, rounded once.  The inverse rotation with the
  * same mscale is also the gradient of y with respect to x.
  * T >= 0 (0 is a no-op), 1 <= H <= 65535, rot even in 2..256, strides >= 0;
  * x, y 2-byte, pos 4-byte and freqs 8-byte aligned.  Rows whose pointers and strides are

@@ -13,9 +13,10 @@ constexpr unsigned kRopeInverse = 0x2u;
 constexpr int kMaxRot = 256;
 
 // (cos, sin) of pos * freq times mscale.  The angle is taken in turns and
-// reduced in double: at position 2^31 the product still has 22 fractional
-// bits more than the fp32 argument keeps, so no position loses accuracy to
-// the reduction.
+// reduced in double.  Its three roundings are off by at most 2.5 * 2^-53 of the
+// turns: below 2^-30 turns up to position 2^24 and so lost in the rounding of the
+// fp32 argument (2^-26 turns), at most 2^-23 turns (7e-7 rad) at position 2^31,
+// where a bf16 result keeps 2^-9.
 __device__ __forceinline__ float2 rope_factors(int pos, double freq, float mscale, bool inverse) {
   const double turns = static_cast<double>(pos) * (freq * 0.15915494309189533576888);  // 1 / (2 pi)
   const float r = static_cast<float>(turns - rint(turns));                               // [-1/2, 1/2]
