@@ -449,8 +449,8 @@ mla_status_t mla_chunk_attend(const void *q, const int32_t *q_offsets, int T,
  * past seq_lens[b] are not written.  The sum is fp32 in an order that depends on the
  * shapes alone.  Bad block ids, lengths and offsets are recorded for
  * mla_cache_get_error; a token whose block id is bad keeps its weight_in.  After
- * MLA_DEVERR_TIMEOUT there some slots are not written.  T >= 0,
- * T * H <= 2^30.
+ * MLA_DEVERR_TIMEOUT there some slots are not written (in place they hold weight_in).
+ * T >= 0, T * H <= 2^30.
  */
 mla_status_t mla_cache_weigh(const void *q, const int32_t *q_offsets, int T, const float *lse,
                              const void *cache, const int32_t *block_table,

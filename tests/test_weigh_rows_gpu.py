@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+from mla_latent_kv_25_b200 import binding
 from oracle import serving
 from tests._serving import SCALE, Chunk
 from tests.test_chunk_gpu import check_weights, weigh
@@ -22,3 +23,33 @@ def test_rows_behind_the_tile_are_not_looked_at(n, H):
     got = weigh(c, good, w.cuda())
     assert torch.equal(got[0], whole[0])
     assert bool(got[1, :69].isnan().all()) and np.all(got[1, 70:].cpu().numpy() == -7.0)
+
+
+@pytest.mark.parametrize("n,lens,H", [([1] * 40, [3000] * 40, 128), ([32], [1024], 128), ([40, 3], [9000, 500], 64)])
+def test_slots_of_a_call_that_gave_up(n, lens, H):
+    """Every slot holds its old weight or the right new one, in place too; the next call is right."""
+    c = Chunk(n, lens, H, seed=7)
+    t = c.cuda()
+    lse = torch.full((c.T, H), 6.0, device="cuda")
+    w = torch.rand(c.B, c.table.shape[1] * 64, generator=torch.Generator().manual_seed(1)).cuda()
+    right = w.clone()
+    binding.mla_cache_weigh(t[0], t[1], lse, t[2], t[3], t[4], SCALE, w, right)
+    assert binding.mla_cache_get_error() == 0
+    some = 0
+    for limit in (1, 1000, 20000):
+        got = w.clone()
+        binding.mla_set_wait_limit(limit)
+        try:
+            binding.mla_cache_weigh(t[0], t[1], lse, t[2], t[3], t[4], SCALE, got, got)
+            bits = binding.mla_cache_get_error()
+        finally:
+            binding.mla_set_wait_limit(0)
+        old, new = got == w, got == right
+        assert bool((old | new).all())
+        left = int((~new).sum())
+        assert bits == binding.DEVERR_TIMEOUT if left else bits in (0, binding.DEVERR_TIMEOUT)
+        some += left
+    assert some > 0, "no wait ran out"
+    got = w.clone()
+    binding.mla_cache_weigh(t[0], t[1], lse, t[2], t[3], t[4], SCALE, got, got)
+    assert binding.mla_cache_get_error() == 0 and torch.equal(got, right)
