@@ -34,10 +34,10 @@
 // bf16 operand of a tensor-core product) while its sum is taken unrounded.
 // Every wait is bounded (WaitCtx).
 //
-// Measured (B200, H = 128): 16 tokens over 131072 0.44 ms = 1330 TFLOP/s (0.91
+// Measured (B200, H = 128): 16 tokens over 131072 0.44 ms = 1320 TFLOP/s (0.90
 // of what 132 SMs can reach at the measured bf16 peak); 512 tokens over 16384
-// 1.64 ms = 1400 TFLOP/s (up to 1.8 ms in a long run under the power cap, at 1.6
-// GHz).  What remains: 33 clusters of four use 132 of 148 SMs, the start and the
+// 1.49 ms = 1540 TFLOP/s in a short run (0.51 and 1.73 ms in a long one under
+// the power cap, at 1.6 GHz).  What remains: 33 clusters of four use 132 of 148 SMs, the start and the
 // end of a tile (about eight blocks' time), and the merge.
 #include <cuda.h>
 #include <math.h>

@@ -21,8 +21,8 @@
 // evict_move_kernel: bulk copies of whole rows through shared memory, 32 rows
 //   in flight per warp, and behind each row its weight and position.  Bound: HBM,
 //   2304 bytes per moved row.
-// Whole call: 64 x 4096 -> 2048 38.4 us, 4 x 131072 -> 65536 86 us (rows alone
-// at the measured copy bandwidth: 23.5 and 47).
+// Whole call: 64 x 4096 -> 2048 39 us, 4 x 131072 -> 65536 87 us (rows alone at
+// the measured copy bandwidth: 23.5 and 47).
 #include <atomic>
 
 #include "common.cuh"

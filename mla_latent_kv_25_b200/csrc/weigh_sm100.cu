@@ -26,9 +26,9 @@
 // w0: TMA; w1: MMA (one thread of a pair's even CTA), TMEM; w2-5: epilogue,
 // thread = token.
 //
-// Measured (H = 128): 64 sequences x 4096 tokens 63 us (0.75 of the measured
-// copy bandwidth; 0.90 at 16384), 32 queries over 4 x 16384 233 us (0.81 of the
-// measured bf16 peak).
+// Measured (H = 128): 64 sequences x 4096 tokens 65 us (0.75 of the measured
+// copy bandwidth; 0.93 at 16384), 32 queries over 4 x 16384 228 us (0.82 of the
+// measured bf16 peak; 261 us in a long run under the power cap).
 #include <cuda.h>
 #include <math.h>
 
